@@ -264,6 +264,86 @@ mlstm_status mlstm_step(const void* q, const void* k, const void* v, const float
                         int DK, int DV, mlstm_dtype dtype, mlstm_gate_mode gate_mode,
                         mlstm_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Gated delta rule: the sibling cell whose matrix memory is corrected towards
+ * each value instead of added to.  For every (batch, head), t = 1..T, with the
+ * log decay g_t and the writing strength beta_t,
+ *
+ *   y_t = v_t - e^{g_t} C_{t-1}^T k_t
+ *   C_t = e^{g_t} C_{t-1} + k_t (beta_t y_t)^T
+ *   h_t = scale C_t^T q_t
+ *
+ * There is no normaliser and no stabiliser; keys are usually unit vectors and
+ * 0 <= beta <= 1, which keeps the memory bounded.
+ *   Q, K [B, NHK, T, DK] and V, H [B, NH, T, DV] in `dtype`; NHK divides NH
+ *   and value head n reads head n / (NH / NHK) of Q and K;
+ *   g, beta [B, NH, T] fp32: g <= 0 (values below -1000, -inf among them, act
+ *   as -1000: the state is forgotten entirely, which starts a new sequence
+ *   inside a row); beta = 0 writes nothing, so g = beta = 0 on padded tokens
+ *   leaves the state as it was;
+ *   C0 (nullable: zero), C_T (nullable) [B, NH, DK, DV] fp32.
+ * Contiguous; 16-byte aligned but for g, beta and their gradients (4 bytes).
+ * Sizes: B, NHK, NH >= 1, T >= 0 (up to 2^22), DK, DV in [1, 1024], B * NH up
+ * to 65535.  T = 0 copies C0 (or zero) to C_T.
+ * Algorithms: SIMT (any size and type, fp32 throughout) and TC (bf16, DK up to
+ * 128, DK and DV multiples of 8; tensor cores, every fp32 operand split into
+ * two bf16 terms so that fp32 outputs keep about 17 bits); AUTO takes TC where
+ * it applies.  Errors as mlstm_fw().
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of workspace of mlstm_gated_delta_fw (backward = 0) or
+ * mlstm_gated_delta_bw (backward = 1). */
+mlstm_status mlstm_gated_delta_workspace_size(int B, int NHK, int NH, int T, int DK, int DV,
+                                              mlstm_dtype dtype, mlstm_algo algo, int backward,
+                                              size_t* bytes);
+
+mlstm_status mlstm_gated_delta_fw(const void* Q, const void* K, const void* V, const float* g,
+                                  const float* beta, const float* C0, void* H, float* C_T, int B,
+                                  int NHK, int NH, int T, int DK, int DV, float scale,
+                                  mlstm_dtype dtype, mlstm_algo algo, void* workspace,
+                                  size_t workspace_bytes, mlstm_stream_t stream);
+
+/* Gradients of a loss on H (dH in `dtype`) and, where dC_T is given (fp32,
+ * nullable), on the final state: dQ, dK [B, NHK, T, DK] (summed over the value
+ * heads that share a key head) and dV in `dtype`; dg, dbeta [B, NH, T] fp32;
+ * dC0 fp32 (nullable).  The forward is recomputed from the inputs.  T = 0
+ * copies dC_T (or zero) to dC0. */
+mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, const float* g,
+                                  const float* beta, const float* C0, const void* dH,
+                                  const float* dC_T, void* dQ, void* dK, void* dV, float* dg,
+                                  float* dbeta, float* dC0, int B, int NHK, int NH, int T, int DK,
+                                  int DV, float scale, mlstm_dtype dtype, mlstm_algo algo,
+                                  void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
+
+/* Single token (decode): advances C in place and writes h.  q, k [B, NHK, DK],
+ * v, h [B, NH, DV] in `dtype`; g, beta [B, NH]; C [B, NH, DK, DV] fp32,
+ * 16-byte aligned (the others by their element).  One launch, no workspace. */
+mlstm_status mlstm_gated_delta_step(const void* q, const void* k, const void* v, const float* g,
+                                    const float* beta, float* C, void* h, int B, int NHK, int NH,
+                                    int DK, int DV, float scale, mlstm_dtype dtype,
+                                    mlstm_stream_t stream);
+
+/* Layer norm of the cell output, per (token, head) over D, into the
+ * token-major layout that an output projection reads:
+ *   X [B, NH, T, D] dtype, weight [NH, D] fp32, bias [NH, D] fp32 (nullable)
+ *   -> Y [B, T, NH * D] dtype; mean, rstd [B, NH, T] fp32 (each nullable):
+ *   Y = (X - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps).
+ * With NH = 1 it is the layer norm of B * T rows.  D in [1, 8192], B * NH up to
+ * 65535, T up to 2^22; pointers 16-byte aligned; eps >= 0.  One launch. */
+mlstm_status mlstm_head_norm_fw(const void* X, const float* weight, const float* bias, void* Y,
+                                float* mean, float* rstd, int B, int NH, int T, int D, float eps,
+                                mlstm_dtype dtype, mlstm_stream_t stream);
+
+/* Gradients of a loss on Y: dX in `dtype`, dweight and dbias (nullable) [NH, D]
+ * fp32, from X, dY [B, T, NH * D] and the forward's mean and rstd.  The sums of
+ * dweight and dbias run in a fixed order.  Two launches. */
+mlstm_status mlstm_head_norm_bw_workspace_size(int B, int NH, int T, int D, mlstm_dtype dtype,
+                                               size_t* bytes);
+mlstm_status mlstm_head_norm_bw(const void* X, const void* dY, const float* weight,
+                                const float* mean, const float* rstd, void* dX, float* dweight,
+                                float* dbias, int B, int NH, int T, int D, mlstm_dtype dtype,
+                                void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device error word:
  * MLSTM_OK, MLSTM_ERR_TIMEOUT (a bounded wait ran out) or MLSTM_ERR_DEVICE;
  * MLSTM_ERR_CUDA if the synchronisation itself failed. */
@@ -303,7 +383,12 @@ typedef enum {
   MLSTM_KERNEL_STEP = 6,          /* single-token step (1 or 2 launches)       */
   MLSTM_KERNEL_BW = 7,            /* backward pass (10 to 14 launches per call) */
   MLSTM_KERNEL_FW_TRAIN = 8,      /* training forward (4 or 5 launches)        */
-  MLSTM_KERNEL_COUNT = 9
+  MLSTM_KERNEL_GATED_DELTA_FW = 9,    /* gated delta rule, forward             */
+  MLSTM_KERNEL_GATED_DELTA_BW = 10,   /* its gradients                         */
+  MLSTM_KERNEL_GATED_DELTA_STEP = 11, /* its single-token step (1 launch)      */
+  MLSTM_KERNEL_HEAD_NORM_FW = 12,     /* cell-output layer norm (1 launch)     */
+  MLSTM_KERNEL_HEAD_NORM_BW = 13,     /* its gradients (2 launches)            */
+  MLSTM_KERNEL_COUNT = 14
 } mlstm_kernel_id;
 
 /* Total number of kernels this library has enqueued since it was loaded. */

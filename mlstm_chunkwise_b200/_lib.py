@@ -16,11 +16,12 @@ ERR_SCRATCH_TOO_SMALL = 6
 DT_F32, DT_BF16 = 0, 1
 GATE_EXP, GATE_SIGMOID, GATE_SIGMOID_PLAIN = 0, 1, 2
 ALGO_AUTO, ALGO_SIMT, ALGO_TC, ALGO_TC_FUSED = 0, 1, 2, 3
-KERNEL_COUNT = 9
+KERNEL_COUNT = 14
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_f = ctypes.c_float
 
 # name -> (restype, argtypes), in the order of include/mlstm_fw.h
 SIGNATURES = {
@@ -38,6 +39,13 @@ SIGNATURES = {
     "mlstm_fw_train": (_i, [_vp] * 13 + [_sz] + [_i] * 7 + [_vp, _sz, _vp]),
     "mlstm_bw_saved": (_i, [_vp] * 10 + [_sz] + [_vp] * 9 + [_i] * 7 + [_vp, _sz, _vp]),
     "mlstm_step": (_i, [_vp] * 9 + [_i] * 6 + [_vp]),
+    "mlstm_gated_delta_workspace_size": (_i, [_i] * 9 + [ctypes.POINTER(_sz)]),
+    "mlstm_gated_delta_fw": (_i, [_vp] * 8 + [_i] * 6 + [_f, _i, _i, _vp, _sz, _vp]),
+    "mlstm_gated_delta_bw": (_i, [_vp] * 14 + [_i] * 6 + [_f, _i, _i, _vp, _sz, _vp]),
+    "mlstm_gated_delta_step": (_i, [_vp] * 7 + [_i] * 5 + [_f, _i, _vp]),
+    "mlstm_head_norm_fw": (_i, [_vp] * 6 + [_i] * 4 + [_f, _i, _vp]),
+    "mlstm_head_norm_bw_workspace_size": (_i, [_i] * 5 + [ctypes.POINTER(_sz)]),
+    "mlstm_head_norm_bw": (_i, [_vp] * 8 + [_i] * 5 + [_vp, _sz, _vp]),
     "mlstm_last_device_error": (_i, [_vp]),
     "mlstm_last_device_error_word": (ctypes.c_uint32, []),
     "mlstm_set_watchdog": (None, [ctypes.c_uint64]),

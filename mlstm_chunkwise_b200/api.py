@@ -385,3 +385,244 @@ def mlstm_chunkwise(Q, K, V, i_pre, f_pre, C0=None, n0=None, m0=None, *, chunk_s
     H, C_T, n_T, m_T = _MlstmChunkwise.apply(Q, K, V, i_pre, f_pre, C0, n0, m0, chunk_size,
                                              gate_mode, algo, recompute)
     return H, (C_T, n_T, m_T)
+
+
+# ---------------------------------------------------------------------------
+# gated delta rule
+# ---------------------------------------------------------------------------
+def _on(device):
+    """Makes ``device`` current for a call (launches go to its stream)."""
+    return torch.cuda.device(device)
+
+
+def _check_gated_delta(Q, K, V, g, beta, C0, T_dims):
+    """Shapes of a gated delta rule call; T_dims is (T,) or () for one token."""
+    n = 3 + len(T_dims)
+    if Q.dim() != n or V.dim() != n:
+        raise ValueError("Q must be [B, NHK, T, DK] and V [B, NH, T, DV]" if T_dims else
+                         "q must be [B, NHK, DK] and v [B, NH, DV]")
+    B, NHK, DK = Q.shape[0], Q.shape[1], Q.shape[-1]
+    NH, DV = V.shape[1], V.shape[-1]
+    dt, dev = Q.dtype, Q.device
+    if dt not in _DT:
+        raise ValueError(f"unsupported dtype {dt} (float32 or bfloat16)")
+    if NHK < 1 or NH % NHK != 0:
+        raise ValueError(f"the {NH} heads of V must be a multiple of the {NHK} heads of Q and K")
+    _check_tensor("Q", Q, dt, (B, NHK, *T_dims, DK), dev)
+    _check_tensor("K", K, dt, (B, NHK, *T_dims, DK), dev)
+    _check_tensor("V", V, dt, (B, NH, *T_dims, DV), dev)
+    _check_tensor("g", g, torch.float32, (B, NH, *T_dims), dev)
+    _check_tensor("beta", beta, torch.float32, (B, NH, *T_dims), dev)
+    _check_tensor("C0" if T_dims else "C", C0, torch.float32, (B, NH, DK, DV), dev)
+    return B, NHK, NH, DK, DV, dev, dt
+
+
+def gated_delta_workspace_size(B, NHK, NH, T, DK, DV, dtype=torch.bfloat16, algo="auto",
+                               backward=False) -> int:
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.lib().mlstm_gated_delta_workspace_size(
+        B, NHK, NH, T, DK, DV, _DT[dtype], _ALGO[algo], int(backward), ctypes.byref(n)),
+        "mlstm_gated_delta_workspace_size")
+    return int(n.value)
+
+
+def gated_delta_fw(Q, K, V, g, beta, C0=None, *, scale: float | None = None, algo: str = "auto",
+                   return_last_state: bool = True, workspace: torch.Tensor | None = None,
+                   out: dict | None = None):
+    """Gated delta rule forward pass on the GPU: for every (b, head) and token,
+
+        C_t = e^{g_t} C_{t-1} + beta_t k_t (v_t - e^{g_t} C_{t-1}^T k_t)^T
+        h_t = scale * C_t^T q_t
+
+    Q, K [B,NHK,T,DK] and V [B,NH,T,DV] (float32 or bfloat16, same dtype), NHK
+    dividing NH: head n of V reads head n // (NH // NHK) of Q and K.  g (log
+    decay, <= 0; -inf forgets the state) and beta [B,NH,T] float32; optional
+    initial state C0 [B,NH,DK,DV] float32.  ``scale`` defaults to 1/sqrt(DK).
+    Padded tokens with g = beta = 0 (and finite q, k, v) leave the state as it
+    was.  Returns ``(H, C_T)``, or ``H`` without ``return_last_state``.  ``out``
+    may hold preallocated ``H`` / ``C_T`` (C_T may be C0 itself); ``workspace`` a
+    uint8 CUDA tensor of at least ``gated_delta_workspace_size(...)`` bytes.
+    ``algo``: "auto", "simt" or "tc".
+    """
+    if Q.dim() != 4:
+        raise ValueError("Q must be [B, NHK, T, DK] and V [B, NH, T, DV]")
+    T = Q.shape[2]
+    B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(Q, K, V, g, beta, C0, (T,))
+    out = {} if out is None else out
+    H, C_T = out.get("H"), out.get("C_T") if return_last_state else None
+    if H is None:
+        H = torch.empty((B, NH, T, DV), dtype=dt, device=dev)
+    if C_T is None and return_last_state:
+        C_T = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
+    _check_tensor("H", H, dt, (B, NH, T, DV), dev)
+    _check_tensor("C_T", C_T, torch.float32, (B, NH, DK, DV), dev)
+    ws_bytes = gated_delta_workspace_size(B, NHK, NH, T, DK, DV, dt, algo)
+    if workspace is None:
+        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or workspace.numel() < ws_bytes or \
+            workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a uint8 tensor of >= {ws_bytes} bytes on {dev}")
+    with _on(dev):
+        st = _lib.lib().mlstm_gated_delta_fw(
+            _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(C0), _ptr(H), _ptr(C_T), B, NHK,
+            NH, T, DK, DV, DK ** -0.5 if scale is None else float(scale), _DT[dt], _ALGO[algo],
+            _ptr(workspace), workspace.numel(), _stream(dev))
+    _lib.check(st, "mlstm_gated_delta_fw")
+    return (H, C_T) if return_last_state else H
+
+
+def gated_delta_bw(Q, K, V, g, beta, dH, C0=None, dC_T=None, *, scale: float | None = None,
+                   algo: str = "auto"):
+    """Gradients of a loss on ``gated_delta_fw``'s H (dH, in the input dtype)
+    and, with ``dC_T`` [B,NH,DK,DV] float32, on its final state.  Returns a dict
+    with dQ, dK (summed over the value heads that share them) and dV in the
+    input dtype, dg and dbeta float32 and, when C0 is given, dC0 float32.  The
+    forward is recomputed from the inputs."""
+    if Q.dim() != 4:
+        raise ValueError("Q must be [B, NHK, T, DK] and V [B, NH, T, DV]")
+    T = Q.shape[2]
+    B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(Q, K, V, g, beta, C0, (T,))
+    _check_tensor("dH", dH, dt, (B, NH, T, DV), dev)
+    _check_tensor("dC_T", dC_T, torch.float32, (B, NH, DK, DV), dev)
+    out = {"dQ": torch.empty_like(Q), "dK": torch.empty_like(K), "dV": torch.empty_like(V),
+           "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
+    if C0 is not None:
+        out["dC0"] = torch.empty_like(C0)
+    n = gated_delta_workspace_size(B, NHK, NH, T, DK, DV, dt, algo, backward=True)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = _lib.lib().mlstm_gated_delta_bw(
+            _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(C0), _ptr(dH), _ptr(dC_T),
+            _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dg"]),
+            _ptr(out["dbeta"]), _ptr(out.get("dC0")), B, NHK, NH, T, DK, DV,
+            DK ** -0.5 if scale is None else float(scale), _DT[dt], _ALGO[algo], _ptr(ws),
+            ws.numel(), _stream(dev))
+    _lib.check(st, "mlstm_gated_delta_bw")
+    return out
+
+
+def gated_delta_step(q, k, v, g, beta, C, *, scale: float | None = None, h=None):
+    """One token of ``gated_delta_fw`` for every (b, head), in place on the
+    state: q, k [B,NHK,DK], v [B,NH,DV], g, beta [B,NH] float32, C [B,NH,DK,DV]
+    float32 (overwritten).  Returns h [B,NH,DV] in the input dtype (``h`` may be
+    given)."""
+    B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(q, k, v, g, beta, C, ())
+    if h is None:
+        h = torch.empty((B, NH, DV), dtype=dt, device=dev)
+    _check_tensor("h", h, dt, (B, NH, DV), dev)
+    with _on(dev):
+        st = _lib.lib().mlstm_gated_delta_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(C), _ptr(h), B, NHK, NH, DK, DV,
+            DK ** -0.5 if scale is None else float(scale), _DT[dt], _stream(dev))
+    _lib.check(st, "mlstm_gated_delta_step")
+    return h
+
+
+class _GatedDelta(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, V, g, beta, C0, scale, algo):
+        H, C_T = gated_delta_fw(Q, K, V, g, beta, C0, scale=scale, algo=algo)
+        ctx.save_for_backward(Q, K, V, g, beta, C0)
+        ctx.cfg = (scale, algo)
+        ctx.set_materialize_grads(False)
+        return H, C_T
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dH, dC_T):
+        if dH is None and dC_T is None:
+            return (None,) * 8
+        Q, K, V, g, beta, C0 = ctx.saved_tensors
+        scale, algo = ctx.cfg
+        dH = torch.zeros_like(V) if dH is None else dH.contiguous()
+        d = gated_delta_bw(Q, K, V, g, beta, dH, C0, None if dC_T is None else dC_T.contiguous(),
+                           scale=scale, algo=algo)
+        return d["dQ"], d["dK"], d["dV"], d["dg"], d["dbeta"], d.get("dC0"), None, None
+
+
+def gated_delta_chunkwise(Q, K, V, g, beta, C0=None, *, scale: float | None = None,
+                          algo: str = "auto"):
+    """``gated_delta_fw`` that autograd can differentiate: returns ``(H, C_T)``;
+    gradients of losses on H and on C_T reach Q, K, V, g, beta and C0.  (Capture
+    of a backward pass into a CUDA graph: as with any autograd function, not
+    while an eager graph holds the same leaves; differentiate ``x.detach()``.)"""
+    return _GatedDelta.apply(Q, K, V, g, beta, C0, scale, algo)
+
+
+# ---------------------------------------------------------------------------
+# layer norm of the cell output
+# ---------------------------------------------------------------------------
+def _check_head_norm(X, weight, bias):
+    if X.dim() != 4:
+        raise ValueError("X must be [B, NH, T, D]")
+    B, NH, T, D = X.shape
+    if X.dtype not in _DT:
+        raise ValueError(f"unsupported dtype {X.dtype} (float32 or bfloat16)")
+    _check_tensor("X", X, X.dtype, (B, NH, T, D), X.device)
+    _check_tensor("weight", weight, torch.float32, (NH, D), X.device)
+    _check_tensor("bias", bias, torch.float32, (NH, D), X.device)
+    return B, NH, T, D, X.device, X.dtype
+
+
+def head_norm_fw(X, weight, bias=None, *, eps: float = 1e-5, out: torch.Tensor | None = None):
+    """Layer norm of the cell output X [B,NH,T,D] (float32 or bfloat16) over D
+    per (token, head), with weight and optional bias [NH,D] float32, laid out
+    token-major for an output projection.  Returns ``(Y [B,T,NH*D], mean, rstd
+    [B,NH,T] float32)``.  With NH = 1 it is the layer norm of B*T rows."""
+    B, NH, T, D, dev, dt = _check_head_norm(X, weight, bias)
+    Y = torch.empty((B, T, NH * D), dtype=dt, device=dev) if out is None else out
+    _check_tensor("out", Y, dt, (B, T, NH * D), dev)
+    mean = torch.empty((B, NH, T), dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    with _on(dev):
+        st = _lib.lib().mlstm_head_norm_fw(_ptr(X), _ptr(weight), _ptr(bias), _ptr(Y), _ptr(mean),
+                                           _ptr(rstd), B, NH, T, D, float(eps), _DT[dt],
+                                           _stream(dev))
+    _lib.check(st, "mlstm_head_norm_fw")
+    return Y, mean, rstd
+
+
+def head_norm_bw(X, dY, weight, mean, rstd, *, bias: bool = True):
+    """Gradients of a loss on ``head_norm_fw``'s Y, from dY [B,T,NH*D] and the
+    forward's mean and rstd: a dict with dX (input dtype), dweight and, with
+    ``bias``, dbias [NH,D] float32 (summed in a fixed order)."""
+    B, NH, T, D, dev, dt = _check_head_norm(X, weight, None)
+    _check_tensor("dY", dY, dt, (B, T, NH * D), dev)
+    _check_tensor("mean", mean, torch.float32, (B, NH, T), dev)
+    _check_tensor("rstd", rstd, torch.float32, (B, NH, T), dev)
+    out = {"dX": torch.empty_like(X), "dweight": torch.empty_like(weight)}
+    if bias:
+        out["dbias"] = torch.empty_like(weight)
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.lib().mlstm_head_norm_bw_workspace_size(B, NH, T, D, _DT[dt],
+                                                            ctypes.byref(n)),
+               "mlstm_head_norm_bw_workspace_size")
+    ws = torch.empty(max(n.value, 1), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = _lib.lib().mlstm_head_norm_bw(
+            _ptr(X), _ptr(dY), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(out["dX"]),
+            _ptr(out["dweight"]), _ptr(out.get("dbias")), B, NH, T, D, _DT[dt], _ptr(ws),
+            ws.numel(), _stream(dev))
+    _lib.check(st, "mlstm_head_norm_bw")
+    return out
+
+
+class _HeadNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, weight, bias, eps):
+        Y, mean, rstd = head_norm_fw(X, weight, bias, eps=eps)
+        ctx.save_for_backward(X, weight, mean, rstd)
+        ctx.has_bias = bias is not None
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        X, weight, mean, rstd = ctx.saved_tensors
+        d = head_norm_bw(X, dY.contiguous(), weight, mean, rstd, bias=ctx.has_bias)
+        return d["dX"], d["dweight"], d.get("dbias"), None
+
+
+def head_norm(X, weight, bias=None, *, eps: float = 1e-5):
+    """``head_norm_fw`` that autograd can differentiate; returns Y."""
+    return _HeadNorm.apply(X, weight, bias, eps)

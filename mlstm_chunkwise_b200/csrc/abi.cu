@@ -9,6 +9,7 @@
 #include <mutex>
 #include <vector>
 
+#include "abi.h"
 #include "common.cuh"
 #include "device_address.h"
 #include "tc.h"
@@ -216,6 +217,15 @@ cudaError_t launch_family(int id, int n_launch, cudaStream_t st, Fn&& fn) {
 int gate_launches(const Problem& p) { return p.NC > 0 ? 2 : 1; }
 
 }  // namespace
+
+// abi.h
+uint32_t* device_error_word() { return error_word_ptr(); }
+unsigned long long watchdog_polls() { return g_max_polls; }
+mlstm_status run_family(int id, int n_launch, cudaStream_t st, cudaError_t (*fn)(void*),
+                        void* arg) {
+  return from_cuda(launch_family(id, n_launch, st, [&] { return fn(arg); }));
+}
+
 }  // namespace mlstm
 
 using namespace mlstm;
@@ -269,6 +279,11 @@ const char* mlstm_kernel_name(int id) {
     case MLSTM_KERNEL_STEP: return "step";
     case MLSTM_KERNEL_BW: return "bw";
     case MLSTM_KERNEL_FW_TRAIN: return "fw_train";
+    case MLSTM_KERNEL_GATED_DELTA_FW: return "gated_delta_fw";
+    case MLSTM_KERNEL_GATED_DELTA_BW: return "gated_delta_bw";
+    case MLSTM_KERNEL_GATED_DELTA_STEP: return "gated_delta_step";
+    case MLSTM_KERNEL_HEAD_NORM_FW: return "head_norm_fw";
+    case MLSTM_KERNEL_HEAD_NORM_BW: return "head_norm_bw";
   }
   return "unknown";
 }

@@ -1,0 +1,213 @@
+// C entry points of the gated delta rule and of the cell-output layer norm:
+// argument checks and dispatch.  Every check happens before the first launch.
+#include <math.h>
+
+#include "abi.h"
+#include "gdn.h"
+#include "head_norm.h"
+
+namespace mlstm {
+namespace {
+
+bool valid_dtype(mlstm_dtype dt) { return dt == MLSTM_DT_F32 || dt == MLSTM_DT_BF16; }
+
+mlstm_status gdn_problem(int B, int NHK, int NH, int T, int DK, int DV, float scale,
+                         GdnProblem* out) {
+  if (B < 1 || NHK < 1 || NH < 1 || T < 0 || DK < 1 || DV < 1) return MLSTM_ERR_INVALID_ARG;
+  if (NH % NHK != 0 || !isfinite(scale)) return MLSTM_ERR_INVALID_ARG;
+  if (DK > 1024 || DV > 1024 || T > (1 << 22) || (long long)B * NH > 65535)
+    return MLSTM_ERR_UNSUPPORTED;
+  GdnProblem p{};
+  p.B = B;
+  p.NHK = NHK;
+  p.NH = NH;
+  p.T = T;
+  p.DK = DK;
+  p.DV = DV;
+  p.BH = B * NH;
+  p.group = NH / NHK;
+  p.scale = scale;
+  p.max_polls = watchdog_polls();
+  *out = p;
+  return MLSTM_OK;
+}
+
+mlstm_status gdn_algo(const GdnProblem& p, mlstm_dtype dt, mlstm_algo req, mlstm_algo* out) {
+  if (!valid_dtype(dt)) return MLSTM_ERR_INVALID_ARG;
+  if (req != MLSTM_ALGO_AUTO && req != MLSTM_ALGO_SIMT && req != MLSTM_ALGO_TC &&
+      req != MLSTM_ALGO_TC_FUSED)
+    return MLSTM_ERR_INVALID_ARG;
+  if (req == MLSTM_ALGO_TC || req == MLSTM_ALGO_TC_FUSED) return MLSTM_ERR_UNSUPPORTED;
+  *out = MLSTM_ALGO_SIMT;
+  return MLSTM_OK;
+}
+
+// dst = src, or zero without one.
+mlstm_status copy_or_zero(float* dst, const float* src, size_t n, cudaStream_t st) {
+  if (!dst || dst == src) return MLSTM_OK;
+  const cudaError_t e =
+      src ? cudaMemcpyAsync(dst, src, n * sizeof(float), cudaMemcpyDeviceToDevice, st)
+          : cudaMemsetAsync(dst, 0, n * sizeof(float), st);
+  return e == cudaSuccess ? MLSTM_OK : MLSTM_ERR_CUDA;
+}
+
+mlstm_status norm_problem(int B, int NH, int T, int D, float eps, mlstm_dtype dt,
+                          HeadNormProblem* out) {
+  if (!valid_dtype(dt)) return MLSTM_ERR_INVALID_ARG;
+  if (B < 1 || NH < 1 || T < 0 || D < 1 || !(eps >= 0.f) || !isfinite(eps))
+    return MLSTM_ERR_INVALID_ARG;
+  if (D > kHeadNormMaxD || T > (1 << 22) || (long long)B * NH > 65535)
+    return MLSTM_ERR_UNSUPPORTED;
+  *out = HeadNormProblem{B, NH, T, D, eps};
+  return MLSTM_OK;
+}
+
+template <size_t N>
+bool all_aligned(unsigned n, const void* const (&ptrs)[N]) {
+  for (const void* q : ptrs)
+    if (!is_aligned(q, n)) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace mlstm
+
+using namespace mlstm;
+
+extern "C" {
+
+mlstm_status mlstm_gated_delta_workspace_size(int B, int NHK, int NH, int T, int DK, int DV,
+                                              mlstm_dtype dtype, mlstm_algo algo, int backward,
+                                              size_t* bytes) {
+  if (!bytes) return MLSTM_ERR_INVALID_ARG;
+  GdnProblem p;
+  mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, 1.f, &p);
+  if (s != MLSTM_OK) return s;
+  mlstm_algo a;
+  s = gdn_algo(p, dtype, algo, &a);
+  if (s != MLSTM_OK) return s;
+  *bytes = gdn_simt_workspace(p, backward != 0);
+  return MLSTM_OK;
+}
+
+mlstm_status mlstm_gated_delta_fw(const void* Q, const void* K, const void* V, const float* g,
+                                  const float* beta, const float* C0, void* H, float* C_T, int B,
+                                  int NHK, int NH, int T, int DK, int DV, float scale,
+                                  mlstm_dtype dtype, mlstm_algo algo, void* workspace,
+                                  size_t workspace_bytes, mlstm_stream_t stream) {
+  GdnProblem p;
+  mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
+  if (s != MLSTM_OK) return s;
+  mlstm_algo a;
+  s = gdn_algo(p, dtype, algo, &a);
+  if (s != MLSTM_OK) return s;
+  if (T > 0 && (!Q || !K || !V || !g || !beta || !H)) return MLSTM_ERR_INVALID_ARG;
+  if (!all_aligned(16, {Q, K, V, C0, H, C_T, workspace}) || !all_aligned(4, {g, beta}))
+    return MLSTM_ERR_INVALID_ARG;
+  const size_t need = gdn_simt_workspace(p, false);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MLSTM_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return copy_or_zero(C_T, C0, (size_t)p.BH * DK * DV, st);
+  p.err = device_error_word();
+  if (!p.err) return MLSTM_ERR_CUDA;
+  const GdnInputs x{Q, K, V, g, beta, C0};
+  return run_family(MLSTM_KERNEL_GATED_DELTA_FW, gdn_simt_launches(p, false), st, [&] {
+    return launch_gdn_simt_fw(p, dtype, x, H, C_T, workspace, st);
+  });
+}
+
+mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, const float* g,
+                                  const float* beta, const float* C0, const void* dH,
+                                  const float* dC_T, void* dQ, void* dK, void* dV, float* dg,
+                                  float* dbeta, float* dC0, int B, int NHK, int NH, int T, int DK,
+                                  int DV, float scale, mlstm_dtype dtype, mlstm_algo algo,
+                                  void* workspace, size_t workspace_bytes, mlstm_stream_t stream) {
+  GdnProblem p;
+  mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
+  if (s != MLSTM_OK) return s;
+  mlstm_algo a;
+  s = gdn_algo(p, dtype, algo, &a);
+  if (s != MLSTM_OK) return s;
+  if (T > 0 && (!Q || !K || !V || !g || !beta || !dH || !dQ || !dK || !dV || !dg || !dbeta))
+    return MLSTM_ERR_INVALID_ARG;
+  if (!all_aligned(16, {Q, K, V, C0, dH, dC_T, dQ, dK, dV, dC0, workspace}) ||
+      !all_aligned(4, {g, beta, dg, dbeta}))
+    return MLSTM_ERR_INVALID_ARG;
+  const size_t need = gdn_simt_workspace(p, true);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MLSTM_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return copy_or_zero(dC0, dC_T, (size_t)p.BH * DK * DV, st);
+  p.err = device_error_word();
+  if (!p.err) return MLSTM_ERR_CUDA;
+  const GdnInputs x{Q, K, V, g, beta, C0};
+  const GdnGrads d{dH, dC_T, dQ, dK, dV, dg, dbeta, dC0};
+  return run_family(MLSTM_KERNEL_GATED_DELTA_BW, gdn_simt_launches(p, true), st, [&] {
+    return launch_gdn_simt_bw(p, dtype, x, d, workspace, st);
+  });
+}
+
+mlstm_status mlstm_gated_delta_step(const void* q, const void* k, const void* v, const float* g,
+                                    const float* beta, float* C, void* h, int B, int NHK, int NH,
+                                    int DK, int DV, float scale, mlstm_dtype dtype,
+                                    mlstm_stream_t stream) {
+  GdnProblem p;
+  const mlstm_status s = gdn_problem(B, NHK, NH, 1, DK, DV, scale, &p);
+  if (s != MLSTM_OK) return s;
+  if (!valid_dtype(dtype) || !q || !k || !v || !g || !beta || !C || !h)
+    return MLSTM_ERR_INVALID_ARG;
+  // single elements are read, except of the state: one head's token of a longer
+  // tensor need not start on a 16-byte boundary
+  if (!all_aligned(dtype == MLSTM_DT_BF16 ? 2 : 4, {q, k, v, h}) || !all_aligned(4, {g, beta}) ||
+      !all_aligned(16, {C}))
+    return MLSTM_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return run_family(MLSTM_KERNEL_GATED_DELTA_STEP, 1, st, [&] {
+    return launch_gdn_step(p, dtype, q, k, v, g, beta, C, h, st);
+  });
+}
+
+mlstm_status mlstm_head_norm_fw(const void* X, const float* weight, const float* bias, void* Y,
+                                float* mean, float* rstd, int B, int NH, int T, int D, float eps,
+                                mlstm_dtype dtype, mlstm_stream_t stream) {
+  HeadNormProblem p;
+  const mlstm_status s = norm_problem(B, NH, T, D, eps, dtype, &p);
+  if (s != MLSTM_OK) return s;
+  if (!weight || (T > 0 && (!X || !Y)) || !all_aligned(16, {X, weight, bias, Y, mean, rstd}))
+    return MLSTM_ERR_INVALID_ARG;
+  if (T == 0) return MLSTM_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return run_family(MLSTM_KERNEL_HEAD_NORM_FW, 1, st, [&] {
+    return launch_head_norm_fw(p, dtype, X, weight, bias, Y, mean, rstd, st);
+  });
+}
+
+mlstm_status mlstm_head_norm_bw_workspace_size(int B, int NH, int T, int D, mlstm_dtype dtype,
+                                               size_t* bytes) {
+  HeadNormProblem p;
+  const mlstm_status s = norm_problem(B, NH, T, D, 0.f, dtype, &p);
+  if (s != MLSTM_OK || !bytes) return s != MLSTM_OK ? s : MLSTM_ERR_INVALID_ARG;
+  *bytes = head_norm_bw_workspace(p, dtype);
+  return MLSTM_OK;
+}
+
+mlstm_status mlstm_head_norm_bw(const void* X, const void* dY, const float* weight,
+                                const float* mean, const float* rstd, void* dX, float* dweight,
+                                float* dbias, int B, int NH, int T, int D, mlstm_dtype dtype,
+                                void* workspace, size_t workspace_bytes, mlstm_stream_t stream) {
+  HeadNormProblem p;
+  const mlstm_status s = norm_problem(B, NH, T, D, 0.f, dtype, &p);
+  if (s != MLSTM_OK) return s;
+  if (!weight || !dweight || (T > 0 && (!X || !dY || !mean || !rstd || !dX)))
+    return MLSTM_ERR_INVALID_ARG;
+  if (!all_aligned(16, {X, dY, weight, mean, rstd, dX, dweight, dbias, workspace}))
+    return MLSTM_ERR_INVALID_ARG;
+  if (workspace_bytes < head_norm_bw_workspace(p, dtype) || !workspace)
+    return MLSTM_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return run_family(MLSTM_KERNEL_HEAD_NORM_BW, 2, st, [&] {
+    return launch_head_norm_bw(p, dtype, X, dY, weight, mean, rstd, dX, dweight, dbias, workspace,
+                               st);
+  });
+}
+
+}  // extern "C"
