@@ -4,6 +4,7 @@
 
 #include "abi.h"
 #include "gdn.h"
+#include "gdn_tc.h"
 #include "head_norm.h"
 
 namespace mlstm {
@@ -32,14 +33,24 @@ mlstm_status gdn_problem(int B, int NHK, int NH, int T, int DK, int DV, float sc
   return MLSTM_OK;
 }
 
-mlstm_status gdn_algo(const GdnProblem& p, mlstm_dtype dt, mlstm_algo req, mlstm_algo* out) {
+// Resolves AUTO and checks that the chosen algorithm takes the call.  The rule
+// is one of type and sizes alone, so that the workspace size computed on the
+// host always matches the algorithm a call picks.
+mlstm_status gdn_algo(const GdnProblem& p, mlstm_dtype dt, mlstm_algo req, bool backward,
+                      mlstm_algo* out) {
   if (!valid_dtype(dt)) return MLSTM_ERR_INVALID_ARG;
-  if (req != MLSTM_ALGO_AUTO && req != MLSTM_ALGO_SIMT && req != MLSTM_ALGO_TC &&
-      req != MLSTM_ALGO_TC_FUSED)
-    return MLSTM_ERR_INVALID_ARG;
-  if (req == MLSTM_ALGO_TC || req == MLSTM_ALGO_TC_FUSED) return MLSTM_ERR_UNSUPPORTED;
-  *out = MLSTM_ALGO_SIMT;
-  return MLSTM_OK;
+  const bool tc = dt == MLSTM_DT_BF16 && gdn_tc_supported(p) && !backward;
+  switch (req) {
+    case MLSTM_ALGO_AUTO: *out = tc ? MLSTM_ALGO_TC : MLSTM_ALGO_SIMT; return MLSTM_OK;
+    case MLSTM_ALGO_SIMT: *out = req; return MLSTM_OK;
+    case MLSTM_ALGO_TC: *out = req; return tc ? MLSTM_OK : MLSTM_ERR_UNSUPPORTED;
+    case MLSTM_ALGO_TC_FUSED: return MLSTM_ERR_UNSUPPORTED;
+  }
+  return MLSTM_ERR_INVALID_ARG;
+}
+
+size_t gdn_workspace(const GdnProblem& p, mlstm_algo a, bool backward) {
+  return a == MLSTM_ALGO_TC ? gdn_tc_workspace(p, backward) : gdn_simt_workspace(p, backward);
 }
 
 // dst = src, or zero without one.
@@ -84,9 +95,9 @@ mlstm_status mlstm_gated_delta_workspace_size(int B, int NHK, int NH, int T, int
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, 1.f, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, &a);
+  s = gdn_algo(p, dtype, algo, backward != 0, &a);
   if (s != MLSTM_OK) return s;
-  *bytes = gdn_simt_workspace(p, backward != 0);
+  *bytes = gdn_workspace(p, a, backward != 0);
   return MLSTM_OK;
 }
 
@@ -99,18 +110,22 @@ mlstm_status mlstm_gated_delta_fw(const void* Q, const void* K, const void* V, c
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, &a);
+  s = gdn_algo(p, dtype, algo, false, &a);
   if (s != MLSTM_OK) return s;
   if (T > 0 && (!Q || !K || !V || !g || !beta || !H)) return MLSTM_ERR_INVALID_ARG;
   if (!all_aligned(16, {Q, K, V, C0, H, C_T, workspace}) || !all_aligned(4, {g, beta}))
     return MLSTM_ERR_INVALID_ARG;
-  const size_t need = gdn_simt_workspace(p, false);
+  const size_t need = gdn_workspace(p, a, false);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MLSTM_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) return copy_or_zero(C_T, C0, (size_t)p.BH * DK * DV, st);
   p.err = device_error_word();
   if (!p.err) return MLSTM_ERR_CUDA;
   const GdnInputs x{Q, K, V, g, beta, C0};
+  if (a == MLSTM_ALGO_TC)
+    return run_family(MLSTM_KERNEL_GATED_DELTA_FW, gdn_tc_launches(p, false), st, [&] {
+      return launch_gdn_tc_fw(p, x, H, C_T, workspace, st);
+    });
   return run_family(MLSTM_KERNEL_GATED_DELTA_FW, gdn_simt_launches(p, false), st, [&] {
     return launch_gdn_simt_fw(p, dtype, x, H, C_T, workspace, st);
   });
@@ -126,14 +141,14 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, &a);
+  s = gdn_algo(p, dtype, algo, true, &a);
   if (s != MLSTM_OK) return s;
   if (T > 0 && (!Q || !K || !V || !g || !beta || !dH || !dQ || !dK || !dV || !dg || !dbeta))
     return MLSTM_ERR_INVALID_ARG;
   if (!all_aligned(16, {Q, K, V, C0, dH, dC_T, dQ, dK, dV, dC0, workspace}) ||
       !all_aligned(4, {g, beta, dg, dbeta}))
     return MLSTM_ERR_INVALID_ARG;
-  const size_t need = gdn_simt_workspace(p, true);
+  const size_t need = gdn_workspace(p, a, true);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MLSTM_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) return copy_or_zero(dC0, dC_T, (size_t)p.BH * DK * DV, st);
