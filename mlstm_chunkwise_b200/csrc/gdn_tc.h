@@ -1,5 +1,15 @@
 // Shared pieces of the gated delta rule's tensor-core kernels (bf16 inputs,
-// d_qk up to 128, chunks of 128 tokens; formulas in gdn.h).
+// d_qk up to 128, chunks of L = 128 tokens; formulas in gdn.h).
+//
+// The state entering a chunk obeys a recurrence with one product per chunk,
+//   S' = e^G S + N - M S,   M = K^T (D beta W),  W = Tinv (Lam K),
+//                           N = K^T (D beta U),  U = Tinv V,
+// and the gradient of the state leaving it the transposed one,
+//   dS = e^G dS' + N' - M^T dS',
+//   N' = Q^T (scale Lam dH) - K^T (Lam Tinv^T (beta scale (Gam . QK^T)^T dH)).
+// M, N and N' of all chunks are formed in parallel; only the recurrences run
+// chunk after chunk (gdn_tc_chain.cu), and outputs and gradients are again
+// formed for all chunks in parallel from the stored states.
 //
 // Precision.  Q, K, V and dH are exact bf16 operands.  Every other operand of a
 // product (state, inverse, z, y, the gated score matrices, and their
@@ -20,6 +30,32 @@ constexpr int kGdnL = 128;  // chunk length of the tensor-core path
 
 inline int gdn_tc_chunks(const GdnProblem& p) { return (p.T + kGdnL - 1) / kGdnL; }
 
+// Workspace pieces, per (bh, chunk).  Operand images hold rows of 128 bytes (64
+// columns of one bf16 term, 128-byte swizzle), 128 rows to a block of 16 KB.
+//   gc     float2[128]          inclusive sums of g inside the chunk (hi, lo)
+//   tinv   uint4[32][128]       Tinv by rows as bf16 terms: piece j < 16 holds columns
+//                               8j .. 8j + 7 of hi, j >= 16 those of lo; row r at [j][r],
+//                               so that a warp of row threads reads 512 contiguous bytes.
+//                               Pieces right of the diagonal's 32 x 32 block are not
+//                               written (they are zero).
+//   tinvt  uint4[32][128]       the same of Tinv^T (backward); pieces left of the
+//                               diagonal's block are not written
+//   M      [2 terms][2][16 KB]  image, rows i, columns j in two blocks of 64
+//   N      [value tile] float4[16][128]: columns 4c .. 4c + 3 of row r at [c][r]; N', then
+//                               dz without its part from dS', in the same form
+//   S, dS  [value tile][2 terms][16 KB]  state entering, and gradient of the state
+//                               leaving, the chunk: rows d_qk, 64 value columns
+//   y, dz  [value tile][2 terms][16 KB]  rows are tokens
+struct GdnTcWs {
+  float2* gc;
+  uint4 *tinv, *tinvt;
+  uint8_t *M, *S, *dS, *y, *dz;
+  float4 *N, *dz0;  // dz0 lies in dz: a tile's reader replaces it
+  float *dq, *dk;   // fp32 [BH][T][DK], with shared key heads
+  int NC, nvt;      // chunks, value tiles of 64 columns
+  size_t bytes;
+};
+
 bool gdn_tc_supported(const GdnProblem& p);
 size_t gdn_tc_workspace(const GdnProblem& p, bool backward);
 int gdn_tc_launches(const GdnProblem& p, bool backward);
@@ -28,30 +64,28 @@ cudaError_t launch_gdn_tc_fw(const GdnProblem& p, const GdnInputs& x, void* H, f
 cudaError_t launch_gdn_tc_bw(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, void* ws,
                              cudaStream_t st);
 
-// Workspace pieces, per (bh, chunk):
-//   gc    float2[128]      inclusive sums of g inside the chunk (hi, lo)
-//   tinv  uint4[32][128]   Tinv by rows as bf16 terms: piece j < 16 holds columns
-//                          8j .. 8j + 7 of hi, j >= 16 those of lo; row r at [j][r],
-//                          so that a warp of row threads reads 512 contiguous bytes.
-//                          Pieces right of the diagonal's 32 x 32 block are not
-//                          written (they are zero).
-//   tinvt uint4[32][128]   the same of Tinv^T (backward); pieces left of the
-//                          diagonal's block are not written
-//   y, dz [value tile][2 terms][16 KB]   operand images: 128 token rows of 128
-//                          bytes (64 value columns), 128-byte swizzle
-//   S, dS [value tile][2 terms][16 KB]   operand images of the state entering and
-//                          of the state gradient leaving the chunk: 128 d_qk rows
-//                          of 128 bytes
-struct GdnTcWs {
-  float2* gc;
-  uint4 *tinv, *tinvt;
-  uint8_t *y, *dz, *S, *dS;
-  float *dq, *dk;  // fp32 [BH][T][DK], with shared key heads
-  int NC, nvt;     // chunks, value tiles of 64 columns
-  size_t bytes;
-};
+// The stages, one launch each.
+cudaError_t launch_gdn_tc_prep(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
+                               bool transposed, cudaStream_t st);
+// reverse: the gradient's recurrence, from dC_T (init) to dC0 (fin).
+cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* init, float* fin,
+                                const GdnTcWs& w, cudaStream_t st);
+cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
+                              cudaStream_t st);
 
 namespace tc {
+
+constexpr uint32_t kBlk = 16384;  // bytes of a block: 128 rows x 64 columns of one term
+
+// Operand descriptors: step kk of 16 along the product's inner axis.
+//   kmaj: rows are the outer axis, the inner axis runs along the columns
+//   mnmaj: rows are the inner axis; outer columns past 64 in the next block
+__device__ __forceinline__ uint64_t kmaj(uint32_t img, int kk) {
+  return sdesc_sw128(img + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t mnmaj(uint32_t img, int kk) {
+  return sdesc_sw128(img + kk * 2048, kBlk, 1024);
+}
 
 // The two bf16 terms of eight fp32 values.
 __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
@@ -65,21 +99,180 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
+// The terms of N values, packed in pairs.
+template <int N>
+__device__ __forceinline__ void split_pack(const float* x, uint32_t (&hi)[N / 2],
+                                           uint32_t (&lo)[N / 2]) {
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+    lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
+                        x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+  }
+}
 
-constexpr uint32_t kGdnImage = 16384;  // bytes of one term of an operand image
-
-// Eight values as 16-byte chunk c of row r of an operand image (both terms).
-__device__ __forceinline__ void put8(uint8_t* img, int r, int c, const float* x) {
+// Eight values as 16-byte piece c of row r of a block; the lo term lies `term`
+// bytes behind the hi term.
+__device__ __forceinline__ void put8(uint8_t* img, uint32_t term, int r, int c, const float* x) {
   uint4 hi, lo;
   split8(x, hi, lo);
   *reinterpret_cast<uint4*>(img + sw128_offset(r, c)) = hi;
-  *reinterpret_cast<uint4*>(img + kGdnImage + sw128_offset(r, c)) = lo;
+  *reinterpret_cast<uint4*>(img + term + sw128_offset(r, c)) = lo;
+}
+// Eight bf16 values of a row.
+__device__ __forceinline__ void unpack8(uint4 u, float* x) {
+  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(v[e] << 16);
+    x[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
 // e^{a - b} of two sums of g held as (hi, lo).
 __device__ __forceinline__ float gdn_decay(float2 a, float2 b) {
   return ex2_approx(((a.x - b.x) + (a.y - b.y)) * kLog2e);
+}
+__device__ __forceinline__ float gdn_exp(float2 a) { return expf(a.x + a.y); }
+
+// True in one lane of a converged warp.  The compiler then knows that a single
+// thread is active and keeps descriptors in uniform registers: a product with A
+// in tensor memory and 64 columns issues in 25 cycles and takes 35, against 44
+// and 50 from a thread picked by its index (measured, one block).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The block as one: everything written so far (shared memory, tensor memory) is
+// visible to the products that `issue` starts, and the block waits for them.
+template <class F>
+__device__ __forceinline__ void run_mma(uint32_t bar, uint32_t& phase, bool& ok,
+                                        const Problem& wt, uint32_t site, F&& issue) {
+  fence_proxy_async_smem();
+  tmem_wait_st();
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x < 32 && elect_one()) {
+    tc_fence_after();
+    if (ok) issue();
+    mma_commit(bar);
+  }
+  if (ok) ok = mbar_wait(bar, phase, wt, site);
+  phase ^= 1;
+  tc_fence_after();
+}
+
+// D (+)= A B over an inner axis of 64 * slabs, both operands in shared memory.
+// AT / BT: the operand's rows are the inner axis.
+template <bool AT, bool BT>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int slabs,
+                                       bool fresh) {
+  for (int s = 0; s < slabs; ++s) {
+    const uint32_t as = a + s * (AT ? 8192 : kBlk), bs = b + s * (BT ? 8192 : kBlk);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+      mma_bf16_ss(d, AT ? mnmaj(as, kk) : kmaj(as, kk), BT ? mnmaj(bs, kk) : kmaj(bs, kk), id,
+                  !fresh || s > 0 || kk > 0);
+  }
+}
+
+// Tinv (or Tinv^T) of row r into tensor memory as the A operand: hi in columns
+// [0, 64), lo in [64, 128); thread half h writes term h.  `from`, `to`: the
+// pieces that exist (the rest is zero).
+__device__ __forceinline__ void load_tinv(const uint4* src, int r, int h, int from, int to,
+                                          uint4 (&t)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    t[i] = i >= from && i < to ? src[(h * 16 + i) * 128 + r] : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void put_tinv(uint32_t trow, int h, const uint4 (&t)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v[16] = {t[4 * i].x,     t[4 * i].y,     t[4 * i].z,     t[4 * i].w,
+                            t[4 * i + 1].x, t[4 * i + 1].y, t[4 * i + 1].z, t[4 * i + 1].w,
+                            t[4 * i + 2].x, t[4 * i + 2].y, t[4 * i + 2].z, t[4 * i + 2].w,
+                            t[4 * i + 3].x, t[4 * i + 3].y, t[4 * i + 3].z, t[4 * i + 3].w};
+    tmem_st16(trow + h * 64 + i * 16, v);
+  }
+}
+// D = A B: A in tensor memory at `a` (hi, lo 64 columns behind), 128 inner
+// indexes; B an image of two terms (`term` bytes apart) with inner rows.
+__device__ __forceinline__ void mma_terms3(uint32_t d, uint32_t a, uint32_t b, uint32_t term,
+                                           uint32_t id) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      mma_bf16_ts(d, a + (t == 1 ? 64 : 0) + kk * 8, mnmaj(b + (t == 2 ? term : 0u), kk), id,
+                  (t | kk) != 0);
+}
+__device__ __forceinline__ void mma_terms2(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      mma_bf16_ts(d, a + t * 64 + kk * 8, mnmaj(b, kk), id, (t | kk) != 0);
+}
+
+// 16 / 8 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+// Four 8 x 8 blocks of 16-bit values, transposed: lane i supplies the address of
+// row i % 8 of block i / 8 and gets, of each block, rows 2 (i % 4) and + 1 of
+// column i / 4.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Sums of g inside the chunk by one warp, in 64 bits, four tokens per lane.
+__device__ __forceinline__ void gdn_chunk_sums(const float* g, int n, int lane, float2* gc,
+                                               float2* out) {
+  double x[4], s = 0.;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int t = 4 * lane + e;
+    s += t < n ? (double)fmaxf(g[t], kGdnMinLogDecay) : 0.;
+    x[e] = s;
+  }
+  double incl = s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const double u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const double v = incl - s + x[e];
+    const float hi = (float)v;
+    gc[4 * lane + e] = out[4 * lane + e] = make_float2(hi, (float)(v - hi));
+  }
 }
 
 }  // namespace tc

@@ -1,0 +1,178 @@
+// Gated delta rule, tensor cores: the recurrence over chunks, of the state
+// (S' = e^G S + N - M S) or of its gradient (dS = e^G dS' + N' - M^T dS', from
+// the last chunk to the first).  A CTA owns one (bh, 64 value columns); its
+// 512 row threads keep the state in fp32 registers.  Per chunk: the state goes
+// to shared memory as an operand image (two bf16 terms, which are also what
+// the chunk's other kernels read), one product with M gives X, and the threads
+// update.  M arrives two chunks ahead, N one chunk ahead in registers.
+//
+// The chain image -> product -> registers is what bounds it: 24 products of
+// 128 x 64 x 16 and two passes per chunk, with HBM mostly idle unless more
+// than one wave of CTAs runs.
+//
+// Warps: 0 loads M, 1 issues the products and stores the images, 2..17 rows
+// (four threads per row, 16 columns each).
+#include <cuda.h>
+
+#include "gdn_tc.h"
+
+namespace mlstm {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 512;  // row threads, four to a row
+constexpr int kThreads = 64 + kRows;
+constexpr uint32_t kOffM = 0;                // 2 x 64 KB
+constexpr uint32_t kOffS = 8 * kBlk;         // 2 x 32 KB
+constexpr uint32_t kOffBar = 12 * kBlk;
+constexpr uint32_t kSmem = kOffBar + 64 + 1024;
+enum : uint32_t { kMFull0, kMFull1, kMFree0, kMFree1, kSop, kX, kBars };
+
+template <bool kRev>
+__global__ void __launch_bounds__(kThreads, 1)
+gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restrict__ fin,
+                    GdnTcWs w) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](uint32_t i) { return sbase + kOffBar + 8 * i; };
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 56);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int vt = blockIdx.x, bh = blockIdx.y, NC = w.NC;
+  const int slabs = (p.DK + 63) / 64;
+  // without a final state the last chunk only needs its image
+  const int steps = fin ? NC : NC - 1;
+  const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
+  auto chunk = [&](int i) { return (size_t)bh * NC + (kRev ? NC - 1 - i : i); };
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i == kSop ? kRows : 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32((const void*)slot), 64);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0; i < steps && ok; ++i) {
+        const int b = i & 1;
+        if (i >= 2) ok = mbar_wait(bar(kMFree0 + b), ((i >> 1) - 1) & 1, wt, 0x51);
+        if (!ok) break;
+        mbar_expect_tx(bar(kMFull0 + b), 2 * slabs * kBlk);
+        const uint8_t* src = w.M + chunk(i) * 4 * kBlk;
+        for (int t = 0; t < 2; ++t)
+          bulk_load(sbase + kOffM + (4 * b + 2 * t) * kBlk, src + t * 2 * kBlk, slabs * kBlk,
+                    bar(kMFull0 + b));
+      }
+      // every load has landed before the CTA exits
+      for (int i = steps > 2 ? steps - 2 : 0; ok && i < steps; ++i)
+        ok = mbar_wait(bar(kMFull0 + (i & 1)), (i >> 1) & 1, wt, 0x52);
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      constexpr uint32_t id = idesc_bf16(128, 64, kRev ? 1 : 0, 1);
+      bool ok = true;
+      for (int i = 0; i < NC && ok; ++i) {
+        const int b = i & 1;
+        const uint32_t ma = sbase + kOffM + 4 * b * kBlk, sa = sbase + kOffS + 2 * b * kBlk;
+        if (i < steps) ok = mbar_wait(bar(kMFull0 + b), (i >> 1) & 1, wt, 0x53);
+        ok = ok && mbar_wait(bar(kSop), i & 1, wt, 0x54);
+        tc_fence_after();
+        if (!ok) break;
+        if (i < steps) {
+          mma_ss<kRev, true>(tmem, ma, sa, id, slabs, true);
+          mma_ss<kRev, true>(tmem, ma, sa + kBlk, id, slabs, false);
+          mma_ss<kRev, true>(tmem, ma + 2 * kBlk, sa, id, slabs, false);
+          // the other image has left before X of this chunk lets the rows rewrite it
+          tma_store_wait_read_all();
+          mma_commit(bar(kX));
+          mma_commit(bar(kMFree0 + b));
+        }
+        uint8_t* dst = (kRev ? w.dS : w.S) + (chunk(i) * w.nvt + vt) * 2 * kBlk;
+        bulk_store(dst, sa, slabs * 8192);
+        bulk_store(dst + kBlk, sa + kBlk, slabs * 8192);
+        tma_store_commit();
+      }
+      tma_store_wait_all();
+    }
+  } else {
+    const int q = warp & 3, r = q * 32 + lane, h = (warp - 2) >> 2;
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + h * 16;
+    const int v0 = vt * 64 + h * 16;  // first value column of this thread
+    bool ok = true;
+    float s[16];
+    float4 n[4];
+    float2 gl;
+    auto load = [&](int i) {
+      const float4* src = w.N + ((chunk(i) * w.nvt + vt) * 16 + h * 4) * 128 + r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) n[e] = src[e * 128];
+      gl = w.gc[chunk(i) * kGdnL + kGdnL - 1];
+    };
+    if (steps > 0) load(0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      s[e] = init && r < p.DK && v0 + e < p.DV ? init[((long)bh * p.DK + r) * p.DV + v0 + e] : 0.f;
+    for (int i = 0; i < NC; ++i) {
+      uint8_t* img = smem + kOffS + (i & 1) * 2 * kBlk;
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) put8(img, kBlk, r, h * 2 + cc, s + 8 * cc);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bar(kSop));
+      if (i == steps) break;
+      const float eg = gdn_exp(gl);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[4 * e] = fmaf(eg, s[4 * e], n[e].x);
+        s[4 * e + 1] = fmaf(eg, s[4 * e + 1], n[e].y);
+        s[4 * e + 2] = fmaf(eg, s[4 * e + 2], n[e].z);
+        s[4 * e + 3] = fmaf(eg, s[4 * e + 3], n[e].w);
+      }
+      if (i + 1 < steps) load(i + 1);
+      ok = ok && mbar_wait(bar(kX), i & 1, wt, 0x55);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[16];
+      tmem_ld16(trow, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] -= __uint_as_float(v[e]);
+    }
+    if (fin && ok && r < p.DK)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)  // DV is a multiple of 8
+        if (v0 + e < p.DV)
+          *reinterpret_cast<float4*>(fin + ((long)bh * p.DK + r) * p.DV + v0 + e) =
+              make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 64);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* init, float* fin,
+                                const GdnTcWs& w, cudaStream_t st) {
+  auto kern = reverse ? gdn_tc_chain_kernel<true> : gdn_tc_chain_kernel<false>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(w.nvt, p.BH), kThreads, kSmem, st>>>(p, init, fin, w);
+  return cudaGetLastError();
+}
+
+}  // namespace mlstm
