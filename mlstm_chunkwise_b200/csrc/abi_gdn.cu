@@ -36,10 +36,9 @@ mlstm_status gdn_problem(int B, int NHK, int NH, int T, int DK, int DV, float sc
 // Resolves AUTO and checks that the chosen algorithm takes the call.  The rule
 // is one of type and sizes alone, so that the workspace size computed on the
 // host always matches the algorithm a call picks.
-mlstm_status gdn_algo(const GdnProblem& p, mlstm_dtype dt, mlstm_algo req, bool backward,
-                      mlstm_algo* out) {
+mlstm_status gdn_algo(const GdnProblem& p, mlstm_dtype dt, mlstm_algo req, mlstm_algo* out) {
   if (!valid_dtype(dt)) return MLSTM_ERR_INVALID_ARG;
-  const bool tc = dt == MLSTM_DT_BF16 && gdn_tc_supported(p) && !backward;
+  const bool tc = dt == MLSTM_DT_BF16 && gdn_tc_supported(p);
   switch (req) {
     case MLSTM_ALGO_AUTO: *out = tc ? MLSTM_ALGO_TC : MLSTM_ALGO_SIMT; return MLSTM_OK;
     case MLSTM_ALGO_SIMT: *out = req; return MLSTM_OK;
@@ -95,7 +94,7 @@ mlstm_status mlstm_gated_delta_workspace_size(int B, int NHK, int NH, int T, int
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, 1.f, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, backward != 0, &a);
+  s = gdn_algo(p, dtype, algo, &a);
   if (s != MLSTM_OK) return s;
   *bytes = gdn_workspace(p, a, backward != 0);
   return MLSTM_OK;
@@ -110,7 +109,7 @@ mlstm_status mlstm_gated_delta_fw(const void* Q, const void* K, const void* V, c
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, false, &a);
+  s = gdn_algo(p, dtype, algo, &a);
   if (s != MLSTM_OK) return s;
   if (T > 0 && (!Q || !K || !V || !g || !beta || !H)) return MLSTM_ERR_INVALID_ARG;
   if (!all_aligned(16, {Q, K, V, C0, H, C_T, workspace}) || !all_aligned(4, {g, beta}))
@@ -141,7 +140,7 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, true, &a);
+  s = gdn_algo(p, dtype, algo, &a);
   if (s != MLSTM_OK) return s;
   if (T > 0 && (!Q || !K || !V || !g || !beta || !dH || !dQ || !dK || !dV || !dg || !dbeta))
     return MLSTM_ERR_INVALID_ARG;
@@ -156,6 +155,10 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
   if (!p.err) return MLSTM_ERR_CUDA;
   const GdnInputs x{Q, K, V, g, beta, C0};
   const GdnGrads d{dH, dC_T, dQ, dK, dV, dg, dbeta, dC0};
+  if (a == MLSTM_ALGO_TC)
+    return run_family(MLSTM_KERNEL_GATED_DELTA_BW, gdn_tc_launches(p, true), st, [&] {
+      return launch_gdn_tc_bw(p, x, d, workspace, st);
+    });
   return run_family(MLSTM_KERNEL_GATED_DELTA_BW, gdn_simt_launches(p, true), st, [&] {
     return launch_gdn_simt_bw(p, dtype, x, d, workspace, st);
   });

@@ -191,6 +191,17 @@ GdnTcWs layout(const GdnProblem& p, bool bw, char* base) {
   w.M = take(nc * 4 * tc::kBlk);
   w.N = reinterpret_cast<float4*>(take(tile));
   w.S = take(tile);
+  if (bw) {
+    w.tinvt = reinterpret_cast<uint4*>(take(nc * 32 * 128 * sizeof(uint4)));
+    w.dS = take(tile);
+    w.y = take(tile);
+    w.dz = take(tile);
+    w.dz0 = reinterpret_cast<float4*>(w.dz);
+    if (p.group > 1) {
+      w.dq = reinterpret_cast<float*>(take((size_t)p.BH * p.T * p.DK * sizeof(float)));
+      w.dk = reinterpret_cast<float*>(take((size_t)p.BH * p.T * p.DK * sizeof(float)));
+    }
+  }
   w.bytes = at;
   return w;
 }
@@ -205,7 +216,7 @@ size_t gdn_tc_workspace(const GdnProblem& p, bool backward) {
   return p.T > 0 ? layout(p, backward, nullptr).bytes : 0;
 }
 
-int gdn_tc_launches(const GdnProblem& p, bool backward) { return backward ? 7 + (p.group > 1) : 3; }
+int gdn_tc_launches(const GdnProblem& p, bool backward) { return backward ? 6 + (p.group > 1) : 3; }
 
 cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
                               cudaStream_t st) {
@@ -229,6 +240,18 @@ cudaError_t launch_gdn_tc_fw(const GdnProblem& p, const GdnInputs& x, void* H, f
   if (e != cudaSuccess) return e;
   if ((e = launch_gdn_tc_chain(p, false, x.C0, C_T, w, st)) != cudaSuccess) return e;
   return launch_gdn_tc_out(p, x, H, w, st);
+}
+
+cudaError_t launch_gdn_tc_bw(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, void* ws,
+                             cudaStream_t st) {
+  const GdnTcWs w = layout(p, true, static_cast<char*>(ws));
+  cudaError_t e = launch_gdn_tc_prep(p, x, w, true, st);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_gdn_tc_chain(p, false, x.C0, nullptr, w, st)) != cudaSuccess) return e;
+  if ((e = launch_gdn_tc_dz0(p, x, d, w, st)) != cudaSuccess) return e;
+  if ((e = launch_gdn_tc_chain(p, true, d.dC_T, d.dC0, w, st)) != cudaSuccess) return e;
+  if ((e = launch_gdn_tc_ydz(p, x, d, w, st)) != cudaSuccess) return e;
+  return launch_gdn_tc_grads(p, x, d, w, st);
 }
 
 }  // namespace mlstm

@@ -72,6 +72,13 @@ cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* 
                                 const GdnTcWs& w, cudaStream_t st);
 cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
                               cudaStream_t st);
+cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+                              const GdnTcWs& w, cudaStream_t st);
+cudaError_t launch_gdn_tc_ydz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+                              const GdnTcWs& w, cudaStream_t st);
+// With shared key heads a second launch adds dQ and dK over the value heads.
+cudaError_t launch_gdn_tc_grads(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+                                const GdnTcWs& w, cudaStream_t st);
 
 namespace tc {
 
@@ -155,10 +162,12 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The block as one: everything written so far (shared memory, tensor memory) is
-// visible to the products that `issue` starts, and the block waits for them.
-template <class F>
+// visible to the products that `issue` starts, and the block waits for them
+// (and does `meanwhile` before it waits).
+template <class F, class G>
 __device__ __forceinline__ void run_mma(uint32_t bar, uint32_t& phase, bool& ok,
-                                        const Problem& wt, uint32_t site, F&& issue) {
+                                        const Problem& wt, uint32_t site, F&& issue,
+                                        G&& meanwhile) {
   fence_proxy_async_smem();
   tmem_wait_st();
   tc_fence_before();
@@ -168,9 +177,16 @@ __device__ __forceinline__ void run_mma(uint32_t bar, uint32_t& phase, bool& ok,
     if (ok) issue();
     mma_commit(bar);
   }
+  __syncwarp();
+  meanwhile();
   if (ok) ok = mbar_wait(bar, phase, wt, site);
   phase ^= 1;
   tc_fence_after();
+}
+template <class F>
+__device__ __forceinline__ void run_mma(uint32_t bar, uint32_t& phase, bool& ok,
+                                        const Problem& wt, uint32_t site, F&& issue) {
+  run_mma(bar, phase, ok, wt, site, issue, [] {});
 }
 
 // D (+)= A B over an inner axis of 64 * slabs, both operands in shared memory.

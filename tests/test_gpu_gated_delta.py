@@ -43,7 +43,7 @@ def run_case(algo, kw, backward=True, scale=None):
     H, C_T = api.gated_delta_fw(*(d[n] for n in gd.NAMES), scale=scale, algo=algo)
     H64, C64 = ref.forward(**gd.fp64(x), scale=scale)
     check(algo, {"H": H, "C_T": C_T}, {"H": H64, "C_T": C64})
-    if not backward or algo == "tc":
+    if not backward:
         return
     gen = torch.Generator().manual_seed(kw.get("seed", 0) + 1)
     dH = torch.randn(x["V"].shape, generator=gen).to(x["V"].dtype)
