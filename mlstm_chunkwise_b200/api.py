@@ -7,6 +7,7 @@ status.  Inputs must be CUDA tensors: there is no CPU path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -22,15 +23,18 @@ _ALGO = {"auto": _lib.ALGO_AUTO, "simt": _lib.ALGO_SIMT, "tc": _lib.ALGO_TC,
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the raw handle: a Stream object costs as much as a launch
+    return torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if device.index is None else device.index)
 
 
 def _check_tensor(name, t, dtype, shape, device):
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype is dtype and t.is_contiguous() and
+                     t.get_device() == device.index):  # -1 off the GPU
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
@@ -390,9 +394,12 @@ def mlstm_chunkwise(Q, K, V, i_pre, f_pre, C0=None, n0=None, m0=None, *, chunk_s
 # ---------------------------------------------------------------------------
 # gated delta rule
 # ---------------------------------------------------------------------------
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """Makes ``device`` current for a call (launches go to its stream)."""
-    return torch.cuda.device(device)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _check_gated_delta(Q, K, V, g, beta, C0, T_dims):
@@ -508,8 +515,9 @@ def gated_delta_step(q, k, v, g, beta, C, *, scale: float | None = None, h=None)
     given)."""
     B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(q, k, v, g, beta, C, ())
     if h is None:
-        h = torch.empty((B, NH, DV), dtype=dt, device=dev)
-    _check_tensor("h", h, dt, (B, NH, DV), dev)
+        h = torch.empty_like(v)
+    else:
+        _check_tensor("h", h, dt, (B, NH, DV), dev)
     with _on(dev):
         st = _lib.lib().mlstm_gated_delta_step(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(C), _ptr(h), B, NHK, NH, DK, DV,

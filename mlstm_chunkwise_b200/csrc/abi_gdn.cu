@@ -33,14 +33,23 @@ mlstm_status gdn_problem(int B, int NHK, int NH, int T, int DK, int DV, float sc
   return MLSTM_OK;
 }
 
+// Gradients of fewer head-tokens than this take the fp32 path: dg of a token is
+// one sum over d_qk x d_v terms that may cancel to a hundredth of their size, and
+// with a few tokens nothing averages that out (one token: 2.5e-5 of dg from the
+// two-term operands, 4e-8 in fp32).  Costs 125 in place of 64 us at 4 tokens of 64
+// x 64; from 64 head-tokens on the tensor cores' dg was within 7e-6.
+constexpr long kFewHeadTokens = 64;
+
 // Resolves AUTO and checks that the chosen algorithm takes the call.  The rule
 // is one of type and sizes alone, so that the workspace size computed on the
 // host always matches the algorithm a call picks.
-mlstm_status gdn_algo(const GdnProblem& p, mlstm_dtype dt, mlstm_algo req, mlstm_algo* out) {
+mlstm_status gdn_algo(const GdnProblem& p, mlstm_dtype dt, mlstm_algo req, bool backward,
+                      mlstm_algo* out) {
   if (!valid_dtype(dt)) return MLSTM_ERR_INVALID_ARG;
   const bool tc = dt == MLSTM_DT_BF16 && gdn_tc_supported(p);
+  const bool few = backward && (long)p.BH * p.T < kFewHeadTokens;
   switch (req) {
-    case MLSTM_ALGO_AUTO: *out = tc ? MLSTM_ALGO_TC : MLSTM_ALGO_SIMT; return MLSTM_OK;
+    case MLSTM_ALGO_AUTO: *out = tc && !few ? MLSTM_ALGO_TC : MLSTM_ALGO_SIMT; return MLSTM_OK;
     case MLSTM_ALGO_SIMT: *out = req; return MLSTM_OK;
     case MLSTM_ALGO_TC: *out = req; return tc ? MLSTM_OK : MLSTM_ERR_UNSUPPORTED;
     case MLSTM_ALGO_TC_FUSED: return MLSTM_ERR_UNSUPPORTED;
@@ -94,7 +103,7 @@ mlstm_status mlstm_gated_delta_workspace_size(int B, int NHK, int NH, int T, int
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, 1.f, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, &a);
+  s = gdn_algo(p, dtype, algo, backward != 0, &a);
   if (s != MLSTM_OK) return s;
   *bytes = gdn_workspace(p, a, backward != 0);
   return MLSTM_OK;
@@ -109,7 +118,7 @@ mlstm_status mlstm_gated_delta_fw(const void* Q, const void* K, const void* V, c
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, &a);
+  s = gdn_algo(p, dtype, algo, false, &a);
   if (s != MLSTM_OK) return s;
   if (T > 0 && (!Q || !K || !V || !g || !beta || !H)) return MLSTM_ERR_INVALID_ARG;
   if (!all_aligned(16, {Q, K, V, C0, H, C_T, workspace}) || !all_aligned(4, {g, beta}))
@@ -140,7 +149,7 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
   mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
   if (s != MLSTM_OK) return s;
   mlstm_algo a;
-  s = gdn_algo(p, dtype, algo, &a);
+  s = gdn_algo(p, dtype, algo, true, &a);
   if (s != MLSTM_OK) return s;
   if (T > 0 && (!Q || !K || !V || !g || !beta || !dH || !dQ || !dK || !dV || !dg || !dbeta))
     return MLSTM_ERR_INVALID_ARG;

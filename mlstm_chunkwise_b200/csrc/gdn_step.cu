@@ -15,10 +15,8 @@
 namespace mlstm {
 namespace {
 
-constexpr int kThreads = 256;
-
 __device__ __forceinline__ float4 load_cols(const float* p, int left) {
-  if (left >= 4) return *reinterpret_cast<const float4*>(p);
+  if (left >= 4) return __ldcs(reinterpret_cast<const float4*>(p));
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (left > 0) v.x = p[0];
   if (left > 1) v.y = p[1];
@@ -40,7 +38,7 @@ __device__ __forceinline__ float4 load4(const float* p, int left) {
 template <bool kVec>
 __device__ __forceinline__ void store4(float* p, int left, float4 v) {
   if (kVec) {
-    if (left >= 4) *reinterpret_cast<float4*>(p) = v;
+    if (left >= 4) __stcs(reinterpret_cast<float4*>(p), v);
   } else {
     if (left > 0) p[0] = v.x;
     if (left > 1) p[1] = v.y;
@@ -57,7 +55,7 @@ __device__ __forceinline__ void fma4(float4& a, float s, float4 x) {
 
 // kVec: DV is a multiple of 4 (every row starts on a 16-byte boundary and a
 // lane's four columns are all inside or all outside).
-template <typename T, int kTX, int kRows, bool kVec>
+template <typename T, int kThreads, int kTX, int kRows, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 gdn_step_kernel(GdnProblem p, const T* __restrict__ q, const T* __restrict__ k,
                 const T* __restrict__ v, const float* __restrict__ g,
@@ -141,11 +139,11 @@ gdn_step_kernel(GdnProblem p, const T* __restrict__ q, const T* __restrict__ k,
   }
 }
 
-template <typename T, int kTX, int kRows, bool kVec>
+template <typename T, int kThreads, int kTX, int kRows, bool kVec>
 cudaError_t go(const GdnProblem& p, const void* q, const void* k, const void* v, const float* g,
                const float* beta, float* C, void* h, cudaStream_t st) {
   const size_t smem = ((size_t)(2 * p.DK + 3) / 4 * 4 + 8 * kThreads + kThreads / 32) * 4;
-  gdn_step_kernel<T, kTX, kRows, kVec>
+  gdn_step_kernel<T, kThreads, kTX, kRows, kVec>
       <<<dim3((p.DV + 4 * kTX - 1) / (4 * kTX), p.BH), kThreads, smem, st>>>(
           p, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, beta,
           C, static_cast<T*>(h));
@@ -155,8 +153,8 @@ cudaError_t go(const GdnProblem& p, const void* q, const void* k, const void* v,
 template <typename T>
 cudaError_t step(const GdnProblem& p, const void* q, const void* k, const void* v, const float* g,
                  const float* beta, float* C, void* h, cudaStream_t st) {
-  if (p.DV % 4 != 0) return go<T, 16, 8, false>(p, q, k, v, g, beta, C, h, st);
-  return go<T, 16, 8, true>(p, q, k, v, g, beta, C, h, st);
+  if (p.DV % 4 != 0) return go<T, 128, 8, 8, false>(p, q, k, v, g, beta, C, h, st);
+  return go<T, 128, 8, 8, true>(p, q, k, v, g, beta, C, h, st);
 }
 
 }  // namespace

@@ -76,7 +76,7 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     sbeta[r] = r < n ? beta[(long)bh * p.T + t0 + r] : 0.f;
   }
   uint4 ti[16];
-  load_tinv(w.tinv + cb * 32 * 128, r, h, 0, 4 * (q + 1), ti);
+  load_tinv<true>(w.tinv + cb * 32 * 128, r, h, 0, 4 * (q + 1), ti);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -193,7 +193,8 @@ GdnTcWs layout(const GdnProblem& p, bool bw, char* base) {
   w.S = take(tile);
   if (bw) {
     w.tinvt = reinterpret_cast<uint4*>(take(nc * 32 * 128 * sizeof(uint4)));
-    w.dS = take(tile);
+    w.dS = take(tile / 2 * 3);
+    w.out = reinterpret_cast<float*>(take(nc * w.nvt * 256 * sizeof(float)));
     w.y = take(tile);
     w.dz = take(tile);
     w.dz0 = reinterpret_cast<float4*>(w.dz);

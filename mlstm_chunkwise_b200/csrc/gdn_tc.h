@@ -18,7 +18,11 @@
 // operands drops only lo.lo.  So fp32 outputs (state, gate gradients) keep
 // about 17 bits at two or three tensor-core products in place of one.  A single
 // bf16 rounding of the state or of the inverse would put 2e-3 of noise on
-// every output, and dg, a difference of large sums, off by percents.
+// every output, and dg, a difference of large sums, off by percents.  Where one
+// rounding alone would set the error of an fp32 output, the operand has a third
+// term (24 bits) or the sum is taken in fp32: the last operands of N and N'
+// (final state, dC0), the gradient of the state in K dS', and y against it
+// (dbeta, dg).
 #pragma once
 
 #include "gdn.h"
@@ -33,7 +37,7 @@ inline int gdn_tc_chunks(const GdnProblem& p) { return (p.T + kGdnL - 1) / kGdnL
 // Workspace pieces, per (bh, chunk).  Operand images hold rows of 128 bytes (64
 // columns of one bf16 term, 128-byte swizzle), 128 rows to a block of 16 KB.
 //   gc     float2[128]          inclusive sums of g inside the chunk (hi, lo)
-//   tinv   uint4[32][128]       Tinv by rows as bf16 terms: piece j < 16 holds columns
+//   tinv   uint4[32][128]       Tinv - I by rows as bf16 terms: piece j < 16 holds columns
 //                               8j .. 8j + 7 of hi, j >= 16 those of lo; row r at [j][r],
 //                               so that a warp of row threads reads 512 contiguous bytes.
 //                               Pieces right of the diagonal's 32 x 32 block are not
@@ -43,13 +47,16 @@ inline int gdn_tc_chunks(const GdnProblem& p) { return (p.T + kGdnL - 1) / kGdnL
 //   M      [2 terms][2][16 KB]  image, rows i, columns j in two blocks of 64
 //   N      [value tile] float4[16][128]: columns 4c .. 4c + 3 of row r at [c][r]; N', then
 //                               dz without its part from dS', in the same form
-//   S, dS  [value tile][2 terms][16 KB]  state entering, and gradient of the state
-//                               leaving, the chunk: rows d_qk, 64 value columns
+//   S      [value tile][2 terms][16 KB]  state entering the chunk: rows d_qk, 64 value
+//                               columns
+//   dS     [value tile][3 terms][16 KB]  gradient of the state leaving the chunk
+//   out    float[value tile][2][128]  D_s y_s.(dS'^T k_s) over 32 columns each
 //   y, dz  [value tile][2 terms][16 KB]  rows are tokens
 struct GdnTcWs {
   float2* gc;
   uint4 *tinv, *tinvt;
   uint8_t *M, *S, *dS, *y, *dz;
+  float* out;
   float4 *N, *dz0;  // dz0 lies in dz: a tile's reader replaces it
   float *dq, *dk;   // fp32 [BH][T][DK], with shared key heads
   int NC, nvt;      // chunks, value tiles of 64 columns
@@ -125,6 +132,17 @@ __device__ __forceinline__ void put8(uint8_t* img, uint32_t term, int r, int c, 
   split8(x, hi, lo);
   *reinterpret_cast<uint4*>(img + sw128_offset(r, c)) = hi;
   *reinterpret_cast<uint4*>(img + term + sw128_offset(r, c)) = lo;
+}
+// The third bf16 term of a value.
+__device__ __forceinline__ float third(float x) {
+  x -= __bfloat162float(__float2bfloat16_rn(x));
+  return x - __bfloat162float(__float2bfloat16_rn(x));
+}
+// Eight values, rounded, as a piece of a block.
+__device__ __forceinline__ void put8_one(uint8_t* img, int r, int c, const float* x) {
+  *reinterpret_cast<uint4*>(img + sw128_offset(r, c)) =
+      make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                 pack_bf16x2(x[6], x[7]));
 }
 // Eight bf16 values of a row.
 __device__ __forceinline__ void unpack8(uint4 u, float* x) {
@@ -205,12 +223,22 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
 
 // Tinv (or Tinv^T) of row r into tensor memory as the A operand: hi in columns
 // [0, 64), lo in [64, 128); thread half h writes term h.  `from`, `to`: the
-// pieces that exist (the rest is zero).
+// pieces that exist (the rest is zero).  kOne: with the identity.
+template <bool kOne>
 __device__ __forceinline__ void load_tinv(const uint4* src, int r, int h, int from, int to,
                                           uint4 (&t)[16]) {
+  const uint32_t one = kOne && h == 0 ? 0x3f80u << (16 * (r & 1)) : 0u;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 16; ++i) {
     t[i] = i >= from && i < to ? src[(h * 16 + i) * 128 + r] : make_uint4(0u, 0u, 0u, 0u);
+    if (kOne && i == r >> 3) {
+      const int e = (r >> 1) & 3;
+      t[i].x |= e == 0 ? one : 0u;
+      t[i].y |= e == 1 ? one : 0u;
+      t[i].z |= e == 2 ? one : 0u;
+      t[i].w |= e == 3 ? one : 0u;
+    }
+  }
 }
 __device__ __forceinline__ void put_tinv(uint32_t trow, int h, const uint4 (&t)[16]) {
 #pragma unroll

@@ -112,7 +112,7 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     tmem_st32(trow + h * 64 + 32, v);
   }
   uint4 ti[16];
-  load_tinv(w.tinvt + cb * 32 * 128, r, h, 4 * q, 16, ti);
+  load_tinv<true>(w.tinvt + cb * 32 * 128, r, h, 4 * q, 16, ti);
   run_mma(bar, phase, ok, wt, 0x72, [&] {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -158,6 +158,16 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     mma_ss<true, true>(tmem + 192, qa, ia, idt, 2, false);
     mma_ss<true, true>(tmem + 192, qa, ia + kBlk, idt, 2, false);
   });
+#pragma unroll
+  for (int cc = 0; cc < 4; ++cc) {
+    float x[8];
+    unpack8(dh[cc], x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = third(x[e] * sl);
+    put8_one(img, r, h * 4 + cc, x);
+  }
+  run_mma(bar, phase, ok, wt, 0x6f,
+          [&] { mma_ss<true, true>(tmem + 192, qa, ia, idt, 2, false); });
   tmem_ld32(trow + 192 + h * 32, v);
   tmem_wait_ld();
   put_n(w.N + nb, v);
@@ -170,36 +180,38 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 }
 
 // ---------------------------------------------------------------- y, dz, dV
+constexpr uint32_t kYBar = 7 * kBlk;
+constexpr uint32_t kYSmem = kYBar + 64;
+
 __global__ void __launch_bounds__(kThreads, 2)
 gdn_tc_ydz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
                   const float* __restrict__ beta, const __nv_bfloat16* __restrict__ V,
                   __nv_bfloat16* __restrict__ dV, GdnTcWs w) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   uint8_t *img = smem + 2 * kBlk, *imgd = smem + 4 * kBlk;  // S, z, y; dS', its z, dz
   const uint32_t ka = sbase, ia = sbase + 2 * kBlk, da = sbase + 4 * kBlk;
-  const uint32_t bar_in = sbase + kOffBar, bar = bar_in + 8;
-  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
+  const uint32_t bar_in = sbase + kYBar, bar = bar_in + 8;
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kYBar + 32);
   const int vt = blockIdx.x, c = blockIdx.y, bh = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
   const int t0 = c * kGdnL, n = min(kGdnL, p.T - t0), v0 = vt * 64 + h * 32;
   const int slabs = (p.DK + 63) / 64;
-  const size_t cb = (size_t)bh * w.NC + c, tile = (cb * w.nvt + vt) * 2 * kBlk;
+  const size_t cb = (size_t)bh * w.NC + c, ct = cb * w.nvt + vt,
+               tile = ct * 2 * kBlk;
   const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
 
   if (tid == 0) {
     mbar_init(bar_in, 1);
     mbar_init(bar, 1);
     fence_barrier_init();
-    mbar_expect_tx(bar_in, slabs * (kBlk + 4 * 8192));
+    mbar_expect_tx(bar_in, slabs * (kBlk + 5 * 8192));
     const int kh = gdn_key_head(p, bh);
     for (int s = 0; s < slabs; ++s) tma_load_3d(ka + s * kBlk, &tm_k, s * 64, t0, kh, bar_in);
-    for (int t = 0; t < 2; ++t) {
-      bulk_load(ia + t * kBlk, w.S + tile + t * kBlk, slabs * 8192, bar_in);
-      bulk_load(da + t * kBlk, w.dS + tile + t * kBlk, slabs * 8192, bar_in);
+    for (int t = 0; t < 3; ++t) {
+      if (t < 2) bulk_load(ia + t * kBlk, w.S + tile + t * kBlk, slabs * 8192, bar_in);
+      bulk_load(da + t * kBlk, w.dS + (ct * 3 + t) * kBlk, slabs * 8192, bar_in);
     }
   }
   if (warp == 1) {
@@ -207,7 +219,7 @@ gdn_tc_ydz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
     tmem_relinquish();
   }
   uint4 ti[16];
-  load_tinv(w.tinv + cb * 32 * 128, r, h, 0, 4 * (q + 1), ti);
+  load_tinv<false>(w.tinv + cb * 32 * 128, r, h, 0, 4 * (q + 1), ti);
   const size_t vb = ((size_t)bh * p.T + t0 + r) * p.DV + v0;
   uint4 vrow[4];
 #pragma unroll
@@ -216,7 +228,7 @@ gdn_tc_ydz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
                                          : make_uint4(0u, 0u, 0u, 0u);
   const float2 gr = w.gc[cb * kGdnL + r], gl = w.gc[cb * kGdnL + kGdnL - 1];
   const float bt = r < n ? beta[(long)bh * p.T + t0 + r] : 0.f;
-  const float lam = gdn_exp(gr), dec = bt * gdn_decay(gl, gr);
+  const float lam = gdn_exp(gr), dec = gdn_decay(gl, gr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -230,12 +242,22 @@ gdn_tc_ydz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
     ok = mbar_wait(bar_in, 0, wt, 0x79);
     tc_fence_after();
     if (!ok) return;
-    for (int t = 0; t < 2; ++t) {
-      mma_ss<false, true>(tmem + 128, ka, ia + t * kBlk, id, slabs, t == 0);
+    for (int t = 0; t < 3; ++t) {
+      if (t < 2) mma_ss<false, true>(tmem + 128, ka, ia + t * kBlk, id, slabs, t == 0);
       mma_ss<false, true>(tmem + 192, ka, da + t * kBlk, id, slabs, t == 0);
     }
   });
   uint32_t v[32];
+  tmem_ld32(trow + 192 + h * 32, v);
+  tmem_wait_ld();
+#pragma unroll
+  for (int cc = 0; cc < 4; ++cc) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = bt * dec * __uint_as_float(v[8 * cc + e]);
+    put8(imgd, kBlk, r, h * 4 + cc, x);
+  }
+  float z[32];
   tmem_ld32(trow + 128 + h * 32, v);
   tmem_wait_ld();
 #pragma unroll
@@ -243,28 +265,32 @@ gdn_tc_ydz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
     float x[8];
     unpack8(vrow[cc], x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(-lam, __uint_as_float(v[8 * cc + e]), x[e]);
-    put8(img, kBlk, r, h * 4 + cc, x);
+    for (int e = 0; e < 8; ++e)
+      z[8 * cc + e] = fmaf(-lam, __uint_as_float(v[8 * cc + e]), x[e]);
+    put8(img, kBlk, r, h * 4 + cc, z + 8 * cc);
   }
-  tmem_ld32(trow + 192 + h * 32, v);
-  tmem_wait_ld();
-#pragma unroll
-  for (int cc = 0; cc < 4; ++cc) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = dec * __uint_as_float(v[8 * cc + e]);
-    put8(imgd, kBlk, r, h * 4 + cc, x);
-  }
-  load_tinv(w.tinvt + cb * 32 * 128, r, h, 4 * q, 16, ti);
+  load_tinv<true>(w.tinvt + cb * 32 * 128, r, h, 4 * q, 16, ti);
   run_mma(bar, phase, ok, wt, 0x77, [&] { mma_terms3(tmem + 128, tmem, ia, kBlk, id); });
   put_tinv(trow, h, ti);
-  tmem_ld32(trow + 128 + h * 32, v);
-  tmem_wait_ld();
+  {
+    uint32_t xd[32];
+    tmem_ld32(trow + 128 + h * 32, v);
+    tmem_ld32(trow + 192 + h * 32, xd);
+    tmem_wait_ld();
+    float o = 0.f;
 #pragma unroll
-  for (int cc = 0; cc < 4; ++cc)
-    put8(img, kBlk, r, h * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
+    for (int cc = 0; cc < 4; ++cc) {
+#pragma unroll
+      for (int e = 8 * cc; e < 8 * cc + 8; ++e) {
+        z[e] += __uint_as_float(v[e]);
+        o = fmaf(z[e], __uint_as_float(xd[e]), o);
+      }
+      put8(img, kBlk, r, h * 4 + cc, z + 8 * cc);
+    }
+    w.out[ct * 256 + h * 128 + r] = dec * o;
+  }
   float4 z0[8];
-  const float4* zp = w.dz0 + ((cb * w.nvt + vt) * 16 + h * 8) * 128 + r;
+  const float4* zp = w.dz0 + (ct * 16 + h * 8) * 128 + r;
 #pragma unroll
   for (int e = 0; e < 8; ++e) z0[e] = zp[e * 128];
   run_mma(bar, phase, ok, wt, 0x78, [&] { mma_terms3(tmem + 192, tmem, da, kBlk, id); });
@@ -311,8 +337,8 @@ constexpr uint32_t kGDh = 4 * kBlk, kGDz = 5 * kBlk, kGY = 7 * kBlk, kGS = 9 * k
 constexpr uint32_t kGR = 4 * kBlk, kGE = 8 * kBlk;  // images of Rh beta, Eh beta
 constexpr uint32_t kGGc = 13 * kBlk;
 constexpr uint32_t kGBeta = kGGc + 1024;
-constexpr uint32_t kGRed = kGBeta + 512;          // float[4][4][128]: ent, out, rows, columns
-constexpr uint32_t kGDiag = kGRed + 4 * 4 * 512;  // float[128]
+constexpr uint32_t kGRed = kGBeta + 512;          // float[3][4][128]: ent, rows, columns
+constexpr uint32_t kGDiag = kGRed + 3 * 4 * 512;  // float[128]
 constexpr uint32_t kGDot = kGDiag + 512;          // float[16]
 constexpr uint32_t kGBar = kGDot + 64;
 constexpr uint32_t kGSmem = kGBar + 64 + 1024;
@@ -348,12 +374,12 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
 
   // pieces of value tile vt: dH, y and both gradients' states; or y and dz alone
   auto load_tile = [&](int vt, bool states) {
-    const size_t tile = (cb * w.nvt + vt) * 2 * kBlk;
+    const size_t ct = cb * w.nvt + vt, tile = ct * 2 * kBlk;
     if (states) {
       tma_load_3d(sbase + kGDh, &tm_dh, vt * 64, t0, bh, bar_in);
       for (int t = 0; t < 2; ++t) {
         bulk_load(sbase + kGS + t * kBlk, w.S + tile + t * kBlk, slabs * 8192, bar_in);
-        bulk_load(sbase + kGDs + t * kBlk, w.dS + tile + t * kBlk, slabs * 8192, bar_in);
+        bulk_load(sbase + kGDs + t * kBlk, w.dS + (ct * 3 + t) * kBlk, slabs * 8192, bar_in);
       }
     }
     bulk_load(sbase + kGDz, w.dz + tile, 2 * kBlk, bar_in);
@@ -436,13 +462,13 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
   }
   dot = warp_sum(dot);
   if (lane == 0) sdot[warp] = dot;
-  // rows of q and k against the products with the states; their scaled sums
-  // stay in place as the first terms of dQ and dK
+  // rows of q and k against the products with the entering state; the scaled
+  // products stay in place as the first terms of dQ and dK
   {
-    float ent = 0.f, out = 0.f;
+    float ent = 0.f;
     if (cols) {
-      const float lam = gdn_exp(gr), dec = gdn_decay(gl, gr);
-      const float fq = p.scale * lam, fo = sbeta[r] * dec;
+      const float lam = gdn_exp(gr);
+      const float fq = p.scale * lam, fo = sbeta[r] * gdn_decay(gl, gr);
       uint32_t a[32], b[32];
       auto piece = [&](uint32_t off, int cc, float* x) {
         unpack8(*reinterpret_cast<const uint4*>(smem + off + (h >> 1) * kBlk +
@@ -476,16 +502,13 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
         for (int e = 0; e < 8; ++e) {
           const float y = lam * __uint_as_float(a[8 * cc + e]), o = __uint_as_float(b[8 * cc + e]);
           sz = fmaf(x[e], y, sz);
-          out = fmaf(x[e], o, out);
           a[8 * cc + e] = __float_as_uint(fmaf(fo, o, -y));
         }
       }
       tmem_st32(trow + 256, a);
       ent = s - sz;
-      out *= dec;
     }
     red[h * 128 + r] = ent;
-    red[(4 + h) * 128 + r] = out;
   }
   // dz y^T
   for (int vt = 0; vt < w.nvt; ++vt) {
@@ -566,8 +589,8 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
       col = rh[0];
     }
-    red[(8 + h) * 128 + r] = row;
-    red[(12 + q) * 128 + h * 32 + lane] = col;
+    red[(4 + h) * 128 + r] = row;
+    red[(8 + q) * 128 + h * 32 + lane] = col;
   }
   const uint32_t id_n = idesc_bf16(128, slabs * 64, 0, 1), id_t = idesc_bf16(128, slabs * 64, 1, 1);
   run_mma(
@@ -596,10 +619,10 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             en += red[i * 128 + t];
-            o[e] += red[(4 + i) * 128 + t];
-            rw += red[(8 + i) * 128 + t];
-            cs[e] += red[(12 + i) * 128 + t];
+            rw += red[(4 + i) * 128 + t];
+            cs[e] += red[(8 + i) * 128 + t];
           }
+          for (int i = 0; i < 2 * w.nvt; ++i) o[e] += w.out[(cb * w.nvt * 2 + i) * 128 + t];
           suf[e] = en + (rw - sbeta[t] * cs[e]);
           ssuf += suf[e];
           pre[e] = sbeta[t] * o[e];
@@ -686,9 +709,9 @@ cudaError_t launch_gdn_tc_ydz(const GdnProblem& p, const GdnInputs& x, const Gdn
   if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(
-      gdn_tc_ydz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      gdn_tc_ydz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kYSmem);
   if (e != cudaSuccess) return e;
-  gdn_tc_ydz_kernel<<<dim3(w.nvt, w.NC, p.BH), kThreads, kSmem, st>>>(
+  gdn_tc_ydz_kernel<<<dim3(w.nvt, w.NC, p.BH), kThreads, kYSmem, st>>>(
       tk, p, x.beta, static_cast<const __nv_bfloat16*>(x.V), static_cast<__nv_bfloat16*>(d.dV), w);
   return cudaGetLastError();
 }

@@ -24,15 +24,17 @@ using namespace tc;
 constexpr int kRows = 512;  // row threads, four to a row
 constexpr int kThreads = 64 + kRows;
 constexpr uint32_t kOffM = 0;                // 2 x 64 KB
-constexpr uint32_t kOffS = 8 * kBlk;         // 2 x 32 KB
-constexpr uint32_t kOffBar = 12 * kBlk;
+constexpr uint32_t kOffS = 8 * kBlk;         // 2 x 32 KB (reverse: three terms, 48 KB)
+constexpr uint32_t kOffBar = 14 * kBlk;
 constexpr uint32_t kSmem = kOffBar + 64 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
 enum : uint32_t { kMFull0, kMFull1, kMFree0, kMFree1, kSop, kX, kBars };
 
 template <bool kRev>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restrict__ fin,
                     GdnTcWs w) {
+  constexpr int kTerms = kRev ? 3 : 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -83,7 +85,7 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
       bool ok = true;
       for (int i = 0; i < NC && ok; ++i) {
         const int b = i & 1;
-        const uint32_t ma = sbase + kOffM + 4 * b * kBlk, sa = sbase + kOffS + 2 * b * kBlk;
+        const uint32_t ma = sbase + kOffM + 4 * b * kBlk, sa = sbase + kOffS + kTerms * b * kBlk;
         if (i < steps) ok = mbar_wait(bar(kMFull0 + b), (i >> 1) & 1, wt, 0x53);
         ok = ok && mbar_wait(bar(kSop), i & 1, wt, 0x54);
         tc_fence_after();
@@ -97,9 +99,9 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
           mma_commit(bar(kX));
           mma_commit(bar(kMFree0 + b));
         }
-        uint8_t* dst = (kRev ? w.dS : w.S) + (chunk(i) * w.nvt + vt) * 2 * kBlk;
-        bulk_store(dst, sa, slabs * 8192);
-        bulk_store(dst + kBlk, sa + kBlk, slabs * 8192);
+        uint8_t* dst = (kRev ? w.dS : w.S) + (chunk(i) * w.nvt + vt) * kTerms * kBlk;
+        for (int t = 0; t < kTerms; ++t)
+          bulk_store(dst + t * kBlk, sa + t * kBlk, slabs * 8192);
         tma_store_commit();
       }
       tma_store_wait_all();
@@ -123,9 +125,17 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
     for (int e = 0; e < 16; ++e)
       s[e] = init && r < p.DK && v0 + e < p.DV ? init[((long)bh * p.DK + r) * p.DV + v0 + e] : 0.f;
     for (int i = 0; i < NC; ++i) {
-      uint8_t* img = smem + kOffS + (i & 1) * 2 * kBlk;
+      uint8_t* img = smem + kOffS + (i & 1) * kTerms * kBlk;
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) put8(img, kBlk, r, h * 2 + cc, s + 8 * cc);
+      for (int cc = 0; cc < 2; ++cc) {
+        put8(img, kBlk, r, h * 2 + cc, s + 8 * cc);
+        if (kRev) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = third(s[8 * cc + e]);
+          put8_one(img + 2 * kBlk, r, h * 2 + cc, x);
+        }
+      }
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(bar(kSop));

@@ -236,7 +236,11 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      split_pack<32>(half ? x : b, hi, lo);
+      float y[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        y[e] = 2 * half + h == q && e == lane ? 0.f : (half ? x : b)[e];
+      split_pack<32>(y, hi, lo);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = half * 8 + h * 4 + i;
@@ -251,7 +255,6 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           *reinterpret_cast<uint4*>(img + (2 + half) * kBlk + sw128_offset(r, h * 4 + i)) = ul;
         }
       }
-      float y[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) y[e] = (half ? x : b)[e] * slam[half * 64 + h * 32 + e];
       split_pack<32>(y, hi, lo);
@@ -275,8 +278,8 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     __syncthreads();
   }
-  // the image of D beta (columns in tensor memory)
-  auto put_scaled = [&](int blocks) {
+  // the image of D beta (columns in tensor memory), or its third term
+  auto put_scaled = [&](int blocks, bool rest) {
     for (int s = 0; s < blocks; ++s) {
       uint32_t v[32];
       tmem_ld32(trow + 128 + s * 64 + h * 32, v);
@@ -286,16 +289,22 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = dec * __uint_as_float(v[8 * cc + e]);
-        put8(img + s * kBlk, 2 * kBlk, r, h * 4 + cc, y);
+        if (!rest) {
+          put8(img + s * kBlk, 2 * kBlk, r, h * 4 + cc, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = third(y[e]);
+          put8_one(img + s * kBlk, r, h * 4 + cc, y);
+        }
       }
     }
   };
-  auto kt_mma = [&](uint32_t id) {
-    mma_ss<true, true>(tmem + 128, ka, ra, id, 2, true);
-    mma_ss<true, true>(tmem + 128, ka, ra + 2 * kBlk, id, 2, false);
+  auto kt_mma = [&](uint32_t d, uint32_t id) {
+    mma_ss<true, true>(d, ka, ra, id, 2, true);
+    mma_ss<true, true>(d, ka, ra + 2 * kBlk, id, 2, false);
   };
-  put_scaled(slabs);
-  run_mma(bar, phase, ok, wt, 0x48, [&] { kt_mma(nkt); });
+  put_scaled(slabs, false);
+  run_mma(bar, phase, ok, wt, 0x48, [&] { kt_mma(tmem + 128, nkt); });
   for (int s = 0; s < slabs; ++s) {
     uint32_t v[32];
     tmem_ld32(trow + 128 + s * 64 + h * 32, v);
@@ -303,14 +312,6 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc)
       put8(img + s * kBlk, 2 * kBlk, r, h * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
-  }
-  // unscaled Tinv for U
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t hi[16], lo[16];
-    split_pack<32>(half ? x : b, hi, lo);
-    tmem_st16(trow + half * 32 + h * 16, hi);
-    tmem_st16(trow + 64 + half * 32 + h * 16, lo);
   }
   fence_proxy_async_smem();
   __syncthreads();
@@ -329,17 +330,26 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       for (int s = 0; s < tiles; ++s)
         tma_load_3d(ra + s * kBlk, &tm_v, (v0 + s) * 64, t0, bh, bar_v);
     }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // Tinv, which N replaces
+      uint32_t hi[16], lo[16];
+      split_pack<32>(half ? x : b, hi, lo);
+      tmem_st16(trow + half * 32 + h * 16, hi);
+      tmem_st16(trow + 64 + half * 32 + h * 16, lo);
+    }
     const uint32_t nv = idesc_bf16(128, tiles * 64, 0, 1), nvt = idesc_bf16(128, tiles * 64, 1, 1);
     run_mma(bar, phase, ok, wt, 0x49, [&] {
       ok = mbar_wait(bar_v, (v0 >> 1) & 1, wt, 0x4a);
       tc_fence_after();
       if (ok) mma_terms2(tmem + 128, tmem, ra, nv);
     });
-    put_scaled(tiles);
-    run_mma(bar, phase, ok, wt, 0x4b, [&] { kt_mma(nvt); });
+    put_scaled(tiles, false);
+    run_mma(bar, phase, ok, wt, 0x4b, [&] { kt_mma(tmem, nvt); });
+    put_scaled(tiles, true);
+    run_mma(bar, phase, ok, wt, 0x4c, [&] { mma_ss<true, true>(tmem, ka, ra, nvt, 2, false); });
     for (int s = 0; s < tiles; ++s) {
       uint32_t v[32];
-      tmem_ld32(trow + 128 + s * 64 + h * 32, v);
+      tmem_ld32(trow + s * 64 + h * 32, v);
       tmem_wait_ld();
       float4* dst = w.N + ((cb * w.nvt + v0 + s) * 16 + h * 8) * 128 + r;
 #pragma unroll
