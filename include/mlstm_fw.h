@@ -287,8 +287,9 @@ mlstm_status mlstm_step(const void* q, const void* k, const void* v, const float
  * to 65535.  T = 0 copies C0 (or zero) to C_T.
  * Algorithms: SIMT (any size and type, fp32 throughout) and TC (bf16, DK up to
  * 128, DK and DV multiples of 8; tensor cores, every fp32 operand split into
- * two bf16 terms so that fp32 outputs keep about 17 bits); AUTO takes TC where
- * it applies.  Errors as mlstm_fw().
+ * two or three bf16 terms so that fp32 outputs keep about 17 bits); AUTO takes
+ * TC where it applies, but SIMT for the gradients of fewer than 64 tokens over
+ * all heads.  Errors as mlstm_fw().
  * ------------------------------------------------------------------------ */
 
 /* Bytes of workspace of mlstm_gated_delta_fw (backward = 0) or
@@ -314,6 +315,33 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
                                   float* dbeta, float* dC0, int B, int NHK, int NH, int T, int DK,
                                   int DV, float scale, mlstm_dtype dtype, mlstm_algo algo,
                                   void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
+
+/* Training pair: mlstm_gated_delta_fw_train is the forward (AUTO's, same
+ * results) that also keeps, in a caller buffer `saved`, what it formed per 128
+ * tokens (sums of g, inverses, transition matrices, states and y, about 2.1 KB
+ * per token and head at DK = DV = 128); mlstm_gated_delta_bw_saved is
+ * mlstm_gated_delta_bw from it, without recomputing the forward.  `saved` must
+ * not change between the two calls.  Only where AUTO takes the tensor cores for
+ * the gradients (else MLSTM_ERR_UNSUPPORTED, from
+ * mlstm_gated_delta_train_sizes first; T = 0 is one such case), which gives the
+ * bytes of `saved` and of each call's workspace.  All three 16-byte aligned. */
+mlstm_status mlstm_gated_delta_train_sizes(int B, int NHK, int NH, int T, int DK, int DV,
+                                           mlstm_dtype dtype, size_t* saved_bytes,
+                                           size_t* fw_workspace_bytes,
+                                           size_t* bw_workspace_bytes);
+mlstm_status mlstm_gated_delta_fw_train(const void* Q, const void* K, const void* V,
+                                        const float* g, const float* beta, const float* C0,
+                                        void* H, float* C_T, void* saved, size_t saved_bytes,
+                                        int B, int NHK, int NH, int T, int DK, int DV, float scale,
+                                        mlstm_dtype dtype, void* workspace, size_t workspace_bytes,
+                                        mlstm_stream_t stream);
+mlstm_status mlstm_gated_delta_bw_saved(const void* Q, const void* K, const void* V,
+                                        const float* g, const float* beta, const void* saved,
+                                        size_t saved_bytes, const void* dH, const float* dC_T,
+                                        void* dQ, void* dK, void* dV, float* dg, float* dbeta,
+                                        float* dC0, int B, int NHK, int NH, int T, int DK, int DV,
+                                        float scale, mlstm_dtype dtype, void* workspace,
+                                        size_t workspace_bytes, mlstm_stream_t stream);
 
 /* Single token (decode): advances C in place and writes h.  q, k [B, NHK, DK],
  * v, h [B, NH, DV] in `dtype`; g, beta [B, NH]; C [B, NH, DK, DV] fp32,

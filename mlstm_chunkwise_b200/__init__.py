@@ -8,7 +8,8 @@ The computation runs in ``libmlstm_fw.so`` (hand-written CUDA kernels; see
 synthetic inputs (``inputs.py``).
 """
 from .api import (MlstmError, gated_delta_bw, gated_delta_chunkwise,  # noqa: F401
-                  gated_delta_fw, gated_delta_step, gated_delta_workspace_size, head_norm,
+                  gated_delta_bw_saved, gated_delta_fw, gated_delta_fw_train, gated_delta_step,
+                  gated_delta_train_sizes, gated_delta_workspace_size, head_norm,
                   head_norm_bw, head_norm_fw, substep_workspace_size, last_device_error, mlstm_bw,
                   mlstm_bw_saved, mlstm_chunkwise, mlstm_fw, mlstm_fw_chunk_states,
                   mlstm_fw_parallel, mlstm_fw_train, mlstm_step, set_watchdog, train_sizes,

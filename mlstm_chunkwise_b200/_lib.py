@@ -42,6 +42,10 @@ SIGNATURES = {
     "mlstm_gated_delta_workspace_size": (_i, [_i] * 9 + [ctypes.POINTER(_sz)]),
     "mlstm_gated_delta_fw": (_i, [_vp] * 8 + [_i] * 6 + [_f, _i, _i, _vp, _sz, _vp]),
     "mlstm_gated_delta_bw": (_i, [_vp] * 14 + [_i] * 6 + [_f, _i, _i, _vp, _sz, _vp]),
+    "mlstm_gated_delta_train_sizes": (_i, [_i] * 7 + [ctypes.POINTER(_sz)] * 3),
+    "mlstm_gated_delta_fw_train": (_i, [_vp] * 9 + [_sz] + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
+    "mlstm_gated_delta_bw_saved": (_i, [_vp] * 6 + [_sz] + [_vp] * 8 + [_i] * 6 +
+                                   [_f, _i, _vp, _sz, _vp]),
     "mlstm_gated_delta_step": (_i, [_vp] * 7 + [_i] * 5 + [_f, _i, _vp]),
     "mlstm_head_norm_fw": (_i, [_vp] * 6 + [_i] * 4 + [_f, _i, _vp]),
     "mlstm_head_norm_bw_workspace_size": (_i, [_i] * 5 + [ctypes.POINTER(_sz)]),

@@ -478,6 +478,17 @@ def gated_delta_fw(Q, K, V, g, beta, C0=None, *, scale: float | None = None, alg
     return (H, C_T) if return_last_state else H
 
 
+def _gated_delta_grads(Q, K, V, g, beta, dH, C0, dC_T):
+    """Checks the upstream gradients and allocates the gradients."""
+    _check_tensor("dH", dH, Q.dtype, tuple(V.shape), Q.device)
+    _check_tensor("dC_T", dC_T, torch.float32, (*V.shape[:2], Q.shape[3], V.shape[3]), Q.device)
+    out = {"dQ": torch.empty_like(Q), "dK": torch.empty_like(K), "dV": torch.empty_like(V),
+           "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
+    if C0 is not None:
+        out["dC0"] = torch.empty_like(C0)
+    return out
+
+
 def gated_delta_bw(Q, K, V, g, beta, dH, C0=None, dC_T=None, *, scale: float | None = None,
                    algo: str = "auto"):
     """Gradients of a loss on ``gated_delta_fw``'s H (dH, in the input dtype)
@@ -489,12 +500,7 @@ def gated_delta_bw(Q, K, V, g, beta, dH, C0=None, dC_T=None, *, scale: float | N
         raise ValueError("Q must be [B, NHK, T, DK] and V [B, NH, T, DV]")
     T = Q.shape[2]
     B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(Q, K, V, g, beta, C0, (T,))
-    _check_tensor("dH", dH, dt, (B, NH, T, DV), dev)
-    _check_tensor("dC_T", dC_T, torch.float32, (B, NH, DK, DV), dev)
-    out = {"dQ": torch.empty_like(Q), "dK": torch.empty_like(K), "dV": torch.empty_like(V),
-           "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
-    if C0 is not None:
-        out["dC0"] = torch.empty_like(C0)
+    out = _gated_delta_grads(Q, K, V, g, beta, dH, C0, dC_T)
     n = gated_delta_workspace_size(B, NHK, NH, T, DK, DV, dt, algo, backward=True)
     ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
     with _on(dev):
@@ -505,6 +511,74 @@ def gated_delta_bw(Q, K, V, g, beta, dH, C0=None, dC_T=None, *, scale: float | N
             DK ** -0.5 if scale is None else float(scale), _DT[dt], _ALGO[algo], _ptr(ws),
             ws.numel(), _stream(dev))
     _lib.check(st, "mlstm_gated_delta_bw")
+    return out
+
+
+def gated_delta_train_sizes(B, NHK, NH, T, DK, DV, dtype=torch.bfloat16):
+    """Bytes of the saved buffer and of the two calls' workspaces of the
+    training pair, or None where it does not exist (it needs the tensor-core
+    gradients: bf16, DK up to 128, DK and DV multiples of 8, at least 64 tokens
+    over all heads)."""
+    sv, fw, bw = ctypes.c_size_t(0), ctypes.c_size_t(0), ctypes.c_size_t(0)
+    st = _lib.lib().mlstm_gated_delta_train_sizes(B, NHK, NH, T, DK, DV, _DT[dtype],
+                                                  ctypes.byref(sv), ctypes.byref(fw),
+                                                  ctypes.byref(bw))
+    if st == _lib.ERR_UNSUPPORTED:
+        return None
+    _lib.check(st, "mlstm_gated_delta_train_sizes")
+    return int(sv.value), int(fw.value), int(bw.value)
+
+
+def gated_delta_fw_train(Q, K, V, g, beta, C0=None, *, scale: float | None = None):
+    """The forward pass of ``gated_delta_fw`` that also keeps what
+    ``gated_delta_bw_saved`` needs.  Returns ``(H, C_T, saved)``; ``saved`` is
+    an opaque uint8 tensor (about 2.1 KB per token and head at DK = DV = 128).
+    Raises ``MlstmError`` (unsupported) outside the shapes of
+    ``gated_delta_train_sizes``."""
+    if Q.dim() != 4:
+        raise ValueError("Q must be [B, NHK, T, DK] and V [B, NH, T, DV]")
+    T = Q.shape[2]
+    B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(Q, K, V, g, beta, C0, (T,))
+    sizes = gated_delta_train_sizes(B, NHK, NH, T, DK, DV, dt)
+    if sizes is None:
+        raise MlstmError(_lib.ERR_UNSUPPORTED, "mlstm_gated_delta_fw_train")
+    H = torch.empty_like(V)
+    C_T = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
+    saved = torch.empty(sizes[0], dtype=torch.uint8, device=dev)
+    ws = torch.empty(sizes[1], dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = _lib.lib().mlstm_gated_delta_fw_train(
+            _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(C0), _ptr(H), _ptr(C_T),
+            _ptr(saved), sizes[0], B, NHK, NH, T, DK, DV,
+            DK ** -0.5 if scale is None else float(scale), _DT[dt], _ptr(ws), sizes[1],
+            _stream(dev))
+    _lib.check(st, "mlstm_gated_delta_fw_train")
+    return H, C_T, saved
+
+
+def gated_delta_bw_saved(Q, K, V, g, beta, saved, dH, C0=None, dC_T=None, *,
+                         scale: float | None = None):
+    """``gated_delta_bw`` from the saved buffer of ``gated_delta_fw_train``
+    (same inputs and scale) instead of a recomputed forward.  Returns the same
+    dict."""
+    if Q.dim() != 4:
+        raise ValueError("Q must be [B, NHK, T, DK] and V [B, NH, T, DV]")
+    T = Q.shape[2]
+    B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(Q, K, V, g, beta, C0, (T,))
+    sizes = gated_delta_train_sizes(B, NHK, NH, T, DK, DV, dt)
+    if sizes is None:
+        raise MlstmError(_lib.ERR_UNSUPPORTED, "mlstm_gated_delta_bw_saved")
+    _check_tensor("saved", saved, torch.uint8, (sizes[0],), dev)
+    out = _gated_delta_grads(Q, K, V, g, beta, dH, C0, dC_T)
+    ws = torch.empty(sizes[2], dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = _lib.lib().mlstm_gated_delta_bw_saved(
+            _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(saved), sizes[0], _ptr(dH),
+            _ptr(dC_T), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out["dg"]),
+            _ptr(out["dbeta"]), _ptr(out.get("dC0")), B, NHK, NH, T, DK, DV,
+            DK ** -0.5 if scale is None else float(scale), _DT[dt], _ptr(ws), sizes[2],
+            _stream(dev))
+    _lib.check(st, "mlstm_gated_delta_bw_saved")
     return out
 
 
@@ -528,9 +602,16 @@ def gated_delta_step(q, k, v, g, beta, C, *, scale: float | None = None, h=None)
 
 class _GatedDelta(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, Q, K, V, g, beta, C0, scale, algo):
-        H, C_T = gated_delta_fw(Q, K, V, g, beta, C0, scale=scale, algo=algo)
-        ctx.save_for_backward(Q, K, V, g, beta, C0)
+    def forward(ctx, Q, K, V, g, beta, C0, scale, algo, recompute):
+        saved = None
+        if not recompute and algo == "auto" and any(ctx.needs_input_grad) and Q.dim() == 4 and \
+                V.dim() == 4 and Q.dtype in _DT and \
+                gated_delta_train_sizes(Q.shape[0], Q.shape[1], V.shape[1], Q.shape[2],
+                                        Q.shape[3], V.shape[3], Q.dtype) is not None:
+            H, C_T, saved = gated_delta_fw_train(Q, K, V, g, beta, C0, scale=scale)
+        else:
+            H, C_T = gated_delta_fw(Q, K, V, g, beta, C0, scale=scale, algo=algo)
+        ctx.save_for_backward(Q, K, V, g, beta, C0, saved)
         ctx.cfg = (scale, algo)
         ctx.set_materialize_grads(False)
         return H, C_T
@@ -539,22 +620,29 @@ class _GatedDelta(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dH, dC_T):
         if dH is None and dC_T is None:
-            return (None,) * 8
-        Q, K, V, g, beta, C0 = ctx.saved_tensors
+            return (None,) * 9
+        Q, K, V, g, beta, C0, saved = ctx.saved_tensors
         scale, algo = ctx.cfg
         dH = torch.zeros_like(V) if dH is None else dH.contiguous()
-        d = gated_delta_bw(Q, K, V, g, beta, dH, C0, None if dC_T is None else dC_T.contiguous(),
-                           scale=scale, algo=algo)
-        return d["dQ"], d["dK"], d["dV"], d["dg"], d["dbeta"], d.get("dC0"), None, None
+        dC_T = None if dC_T is None else dC_T.contiguous()
+        if saved is not None:
+            d = gated_delta_bw_saved(Q, K, V, g, beta, saved, dH, C0, dC_T, scale=scale)
+        else:
+            d = gated_delta_bw(Q, K, V, g, beta, dH, C0, dC_T, scale=scale, algo=algo)
+        return (d["dQ"], d["dK"], d["dV"], d["dg"], d["dbeta"], d.get("dC0"), None, None, None)
 
 
 def gated_delta_chunkwise(Q, K, V, g, beta, C0=None, *, scale: float | None = None,
-                          algo: str = "auto"):
+                          algo: str = "auto", recompute: bool = False):
     """``gated_delta_fw`` that autograd can differentiate: returns ``(H, C_T)``;
-    gradients of losses on H and on C_T reach Q, K, V, g, beta and C0.  (Capture
-    of a backward pass into a CUDA graph: as with any autograd function, not
-    while an eager graph holds the same leaves; differentiate ``x.detach()``.)"""
-    return _GatedDelta.apply(Q, K, V, g, beta, C0, scale, algo)
+    gradients of losses on H and on C_T reach Q, K, V, g, beta and C0.  Where
+    the training pair exists (``gated_delta_train_sizes``) the forward keeps
+    about 2.1 KB per token and head (DK = DV = 128) for the backward;
+    ``recompute=True`` keeps the inputs alone and recomputes the forward.
+    (Capture of a backward pass into a CUDA graph: as with any autograd
+    function, not while an eager graph holds the same leaves; differentiate
+    ``x.detach()``.)"""
+    return _GatedDelta.apply(Q, K, V, g, beta, C0, scale, algo, recompute)
 
 
 # ---------------------------------------------------------------------------

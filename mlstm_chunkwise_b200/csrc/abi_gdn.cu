@@ -61,6 +61,17 @@ size_t gdn_workspace(const GdnProblem& p, mlstm_algo a, bool backward) {
   return a == MLSTM_ALGO_TC ? gdn_tc_workspace(p, backward) : gdn_simt_workspace(p, backward);
 }
 
+// Sizes of the training pair, where AUTO would take the tensor cores for the
+// gradients.
+mlstm_status gdn_train(const GdnProblem& p, mlstm_dtype dt, GdnTrainSizes* z) {
+  mlstm_algo a;
+  const mlstm_status s = gdn_algo(p, dt, MLSTM_ALGO_AUTO, true, &a);
+  if (s != MLSTM_OK) return s;
+  if (a != MLSTM_ALGO_TC) return MLSTM_ERR_UNSUPPORTED;
+  *z = gdn_tc_train_sizes(p);
+  return MLSTM_OK;
+}
+
 // dst = src, or zero without one.
 mlstm_status copy_or_zero(float* dst, const float* src, size_t n, cudaStream_t st) {
   if (!dst || dst == src) return MLSTM_OK;
@@ -170,6 +181,78 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
     });
   return run_family(MLSTM_KERNEL_GATED_DELTA_BW, gdn_simt_launches(p, true), st, [&] {
     return launch_gdn_simt_bw(p, dtype, x, d, workspace, st);
+  });
+}
+
+mlstm_status mlstm_gated_delta_train_sizes(int B, int NHK, int NH, int T, int DK, int DV,
+                                           mlstm_dtype dtype, size_t* saved_bytes,
+                                           size_t* fw_workspace_bytes,
+                                           size_t* bw_workspace_bytes) {
+  if (!saved_bytes || !fw_workspace_bytes || !bw_workspace_bytes) return MLSTM_ERR_INVALID_ARG;
+  GdnProblem p;
+  mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, 1.f, &p);
+  if (s != MLSTM_OK) return s;
+  GdnTrainSizes z;
+  s = gdn_train(p, dtype, &z);
+  if (s != MLSTM_OK) return s;
+  *saved_bytes = z.saved;
+  *fw_workspace_bytes = z.fw;
+  *bw_workspace_bytes = z.bw;
+  return MLSTM_OK;
+}
+
+mlstm_status mlstm_gated_delta_fw_train(const void* Q, const void* K, const void* V,
+                                        const float* g, const float* beta, const float* C0,
+                                        void* H, float* C_T, void* saved, size_t saved_bytes,
+                                        int B, int NHK, int NH, int T, int DK, int DV, float scale,
+                                        mlstm_dtype dtype, void* workspace, size_t workspace_bytes,
+                                        mlstm_stream_t stream) {
+  GdnProblem p;
+  mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
+  if (s != MLSTM_OK) return s;
+  GdnTrainSizes z;
+  s = gdn_train(p, dtype, &z);
+  if (s != MLSTM_OK) return s;
+  if (!Q || !K || !V || !g || !beta || !H || !saved || !workspace) return MLSTM_ERR_INVALID_ARG;
+  if (!all_aligned(16, {Q, K, V, C0, H, C_T, saved, workspace}) || !all_aligned(4, {g, beta}))
+    return MLSTM_ERR_INVALID_ARG;
+  if (saved_bytes < z.saved || workspace_bytes < z.fw) return MLSTM_ERR_INVALID_ARG;
+  p.err = device_error_word();
+  if (!p.err) return MLSTM_ERR_CUDA;
+  const GdnInputs x{Q, K, V, g, beta, C0};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return run_family(MLSTM_KERNEL_GATED_DELTA_FW, gdn_tc_train_launches(p, false), st, [&] {
+    return launch_gdn_tc_fw_train(p, x, H, C_T, saved, workspace, st);
+  });
+}
+
+mlstm_status mlstm_gated_delta_bw_saved(const void* Q, const void* K, const void* V,
+                                        const float* g, const float* beta, const void* saved,
+                                        size_t saved_bytes, const void* dH, const float* dC_T,
+                                        void* dQ, void* dK, void* dV, float* dg, float* dbeta,
+                                        float* dC0, int B, int NHK, int NH, int T, int DK, int DV,
+                                        float scale, mlstm_dtype dtype, void* workspace,
+                                        size_t workspace_bytes, mlstm_stream_t stream) {
+  GdnProblem p;
+  mlstm_status s = gdn_problem(B, NHK, NH, T, DK, DV, scale, &p);
+  if (s != MLSTM_OK) return s;
+  GdnTrainSizes z;
+  s = gdn_train(p, dtype, &z);
+  if (s != MLSTM_OK) return s;
+  if (!Q || !K || !V || !g || !beta || !saved || !dH || !dQ || !dK || !dV || !dg || !dbeta ||
+      !workspace)
+    return MLSTM_ERR_INVALID_ARG;
+  if (!all_aligned(16, {Q, K, V, saved, dH, dC_T, dQ, dK, dV, dC0, workspace}) ||
+      !all_aligned(4, {g, beta, dg, dbeta}))
+    return MLSTM_ERR_INVALID_ARG;
+  if (saved_bytes < z.saved || workspace_bytes < z.bw) return MLSTM_ERR_INVALID_ARG;
+  p.err = device_error_word();
+  if (!p.err) return MLSTM_ERR_CUDA;
+  const GdnInputs x{Q, K, V, g, beta, nullptr};
+  const GdnGrads d{dH, dC_T, dQ, dK, dV, dg, dbeta, dC0};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return run_family(MLSTM_KERNEL_GATED_DELTA_BW, gdn_tc_train_launches(p, true), st, [&] {
+    return launch_gdn_tc_bw_saved(p, x, d, saved, workspace, st);
   });
 }
 

@@ -70,6 +70,16 @@ cudaError_t launch_gdn_tc_fw(const GdnProblem& p, const GdnInputs& x, void* H, f
                              void* ws, cudaStream_t st);
 cudaError_t launch_gdn_tc_bw(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, void* ws,
                              cudaStream_t st);
+// The pair that hands the chunks' sums, inverses, M, states and y on in `saved`.
+struct GdnTrainSizes {
+  size_t saved, fw, bw;
+};
+GdnTrainSizes gdn_tc_train_sizes(const GdnProblem& p);
+int gdn_tc_train_launches(const GdnProblem& p, bool backward);
+cudaError_t launch_gdn_tc_fw_train(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T,
+                                   void* saved, void* ws, cudaStream_t st);
+cudaError_t launch_gdn_tc_bw_saved(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+                                   const void* saved, void* ws, cudaStream_t st);
 
 // The stages, one launch each.
 cudaError_t launch_gdn_tc_prep(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
@@ -77,12 +87,13 @@ cudaError_t launch_gdn_tc_prep(const GdnProblem& p, const GdnInputs& x, const Gd
 // reverse: the gradient's recurrence, from dC_T (init) to dC0 (fin).
 cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* init, float* fin,
                                 const GdnTcWs& w, cudaStream_t st);
+// H may be null (y alone).
 cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
                               cudaStream_t st);
 cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
                               const GdnTcWs& w, cudaStream_t st);
-cudaError_t launch_gdn_tc_ydz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
-                              const GdnTcWs& w, cudaStream_t st);
+cudaError_t launch_gdn_tc_dz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+                             const GdnTcWs& w, cudaStream_t st);
 // With shared key heads a second launch adds dQ and dK over the value heads.
 cudaError_t launch_gdn_tc_grads(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
                                 const GdnTcWs& w, cudaStream_t st);
@@ -222,32 +233,35 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
 }
 
 // Tinv (or Tinv^T) of row r into tensor memory as the A operand: hi in columns
-// [0, 64), lo in [64, 128); thread half h writes term h.  `from`, `to`: the
-// pieces that exist (the rest is zero).  kOne: with the identity.
+// [0, 64), lo in [64, 128).  512 threads: thread h of the row takes pieces
+// 8 (h & 1) .. of term h >> 1 to columns 32 h ...  `from`, `to`: the pieces that
+// exist (the rest is zero).  kOne: with the identity.
 template <bool kOne>
 __device__ __forceinline__ void load_tinv(const uint4* src, int r, int h, int from, int to,
-                                          uint4 (&t)[16]) {
-  const uint32_t one = kOne && h == 0 ? 0x3f80u << (16 * (r & 1)) : 0u;
+                                          uint4 (&t)[8]) {
+  const uint32_t one = kOne && h < 2 ? 0x3f80u << (16 * (r & 1)) : 0u;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    t[i] = i >= from && i < to ? src[(h * 16 + i) * 128 + r] : make_uint4(0u, 0u, 0u, 0u);
+  for (int k = 0; k < 8; ++k) {
+    const int i = (h & 1) * 8 + k;
+    t[k] = i >= from && i < to ? src[((h >> 1) * 16 + i) * 128 + r] : make_uint4(0u, 0u, 0u, 0u);
     if (kOne && i == r >> 3) {
       const int e = (r >> 1) & 3;
-      t[i].x |= e == 0 ? one : 0u;
-      t[i].y |= e == 1 ? one : 0u;
-      t[i].z |= e == 2 ? one : 0u;
-      t[i].w |= e == 3 ? one : 0u;
+      t[k].x |= e == 0 ? one : 0u;
+      t[k].y |= e == 1 ? one : 0u;
+      t[k].z |= e == 2 ? one : 0u;
+      t[k].w |= e == 3 ? one : 0u;
     }
   }
 }
-__device__ __forceinline__ void put_tinv(uint32_t trow, int h, const uint4 (&t)[16]) {
+// trow: the thread's lane and first column.
+__device__ __forceinline__ void put_tinv(uint32_t trow, const uint4 (&t)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const uint32_t v[16] = {t[4 * i].x,     t[4 * i].y,     t[4 * i].z,     t[4 * i].w,
                             t[4 * i + 1].x, t[4 * i + 1].y, t[4 * i + 1].z, t[4 * i + 1].w,
                             t[4 * i + 2].x, t[4 * i + 2].y, t[4 * i + 2].z, t[4 * i + 2].w,
                             t[4 * i + 3].x, t[4 * i + 3].y, t[4 * i + 3].z, t[4 * i + 3].w};
-    tmem_st16(trow + h * 64 + i * 16, v);
+    tmem_st16(trow + i * 16, v);
   }
 }
 // D = A B: A in tensor memory at `a` (hi, lo 64 columns behind), 128 inner

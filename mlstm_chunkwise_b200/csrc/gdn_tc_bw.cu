@@ -1,12 +1,13 @@
 // Gated delta rule on the tensor cores: gradients (formulas in gdn.h).  Three
-// kernels, each for all chunks in parallel, around the two recurrences:
+// kernels, each for all chunks in parallel, around the reverse recurrence:
 //   dz0    Tinv^T (beta scale (Gam . QK^T)^T dH) and N' of the reverse recurrence
-//   ydz    y, dz = dz0 + Tinv^T (beta D K dS') and dV, from both states
+//   dz     dz = dz0 + Tinv^T (beta D K dS') and dV, from the gradient of the state
 //   grads  dQ, dK, dg and dbeta
-// The first two are chains of dependent products with a pass through registers
-// after each, bound by latency: two blocks share an SM.  The third holds one
-// chunk's operands (208 KB) and five 128 x 128 accumulators in turn in all of
-// the tensor memory: about 90 products of 128 x 128 x 64 for 128 value columns.
+// The first two are persistent, one block of 512 threads per SM on up to 128
+// value columns, thread (r, h) on columns 32 h .. of row r: rounds of products
+// with a pass through registers after each.  The third holds one chunk's operands
+// (208 KB) and five 128 x 128 accumulators in turn in all of the tensor memory:
+// about 90 products of 128 x 128 x 64 for 128 value columns.
 #include <cuda.h>
 
 #include "gdn_tc.h"
@@ -16,12 +17,36 @@ namespace {
 
 using namespace tc;
 
+constexpr int kThreads = 512;
+constexpr long kSms = 148;
+
+// (bh, chunk, pair of value tiles) of a persistent kernel's item.
+struct Item {
+  size_t cb;
+  int bh, t0, n, vt, tiles;
+  __device__ Item(long i, const GdnProblem& p, const GdnTcWs& w) {
+    const int pairs = (w.nvt + 1) / 2;
+    cb = (size_t)(i / pairs);
+    vt = (int)(i % pairs) * 2;
+    tiles = min(2, w.nvt - vt);
+    bh = (int)(cb / w.NC);
+    t0 = (int)(cb % w.NC) * kGdnL;
+    n = min(kGdnL, p.T - t0);
+  }
+};
+inline long items_of(const GdnProblem& p, const GdnTcWs& w) {
+  return (long)p.BH * w.NC * ((w.nvt + 1) / 2);
+}
+
 // ---------------------------------------------------------------- dz0, N'
-constexpr int kThreads = 256;
-constexpr uint32_t kOffGc = 6 * kBlk;
-constexpr uint32_t kOffBeta = kOffGc + 1024;
-constexpr uint32_t kOffBar = kOffBeta + 512;
-constexpr uint32_t kSmem = kOffBar + 64 + 1024;
+// Tensor memory: K Q^T then (Gam . QK^T)^T [0, 128), Tinv^T [128, 256), w0 then
+// dz0 [256, 384), N' [384, 512).  The last operand of N', scale Lam dH, has three
+// terms: two go under the first round, the third under the third.
+constexpr uint32_t kZDh = 4 * kBlk, kZL = 6 * kBlk, kZW = 10 * kBlk;
+constexpr uint32_t kZGc = 14 * kBlk;
+constexpr uint32_t kZBar = kZGc + 1024;
+constexpr uint32_t kZSmem = kZBar + 64 + 1024;
+static_assert(kZSmem <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ void put_n(float4* dst, const uint32_t (&v)[32]) {
 #pragma unroll
@@ -30,7 +55,7 @@ __device__ __forceinline__ void put_n(float4* dst, const uint32_t (&v)[32]) {
                                __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
 gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_dh, GdnProblem p,
                   const float* __restrict__ beta, GdnTcWs w) {
@@ -38,288 +63,326 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  float2* gc = reinterpret_cast<float2*>(smem + kOffGc);
-  uint8_t* img = smem + 4 * kBlk;  // dH, then the operands made of it (two terms)
-  const uint32_t qa = sbase, ka = sbase + 2 * kBlk, ia = sbase + 4 * kBlk;
-  const uint32_t bar_in = sbase + kOffBar, bar = bar_in + 8;
-  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
-  const int vt = blockIdx.x, c = blockIdx.y, bh = blockIdx.z;
+  float2* gc = reinterpret_cast<float2*>(smem + kZGc);
+  const uint32_t qa = sbase, ka = sbase + 2 * kBlk, ha = sbase + kZDh, la = sbase + kZL,
+                 wa = sbase + kZW;
+  const uint32_t bar_qk = sbase + kZBar, bar_h = bar_qk + 8, bar = bar_qk + 16;
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kZBar + 32);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
-  const int t0 = c * kGdnL, n = min(kGdnL, p.T - t0);
   const int slabs = (p.DK + 63) / 64;
-  const size_t cb = (size_t)bh * w.NC + c;
+  const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
   const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
+  auto load_qk = [&](const Item& x) {
+    mbar_expect_tx(bar_qk, 2 * slabs * kBlk);
+    const int kh = gdn_key_head(p, x.bh);
+    for (int s = 0; s < slabs; ++s) {
+      tma_load_3d(ka + s * kBlk, &tm_k, s * 64, x.t0, kh, bar_qk);
+      tma_load_3d(qa + s * kBlk, &tm_q, s * 64, x.t0, kh, bar_qk);
+    }
+  };
+  auto load_dh = [&](const Item& x) {
+    mbar_expect_tx(bar_h, x.tiles * kBlk);
+    for (int v = 0; v < x.tiles; ++v)
+      tma_load_3d(ha + v * kBlk, &tm_dh, (x.vt + v) * 64, x.t0, x.bh, bar_h);
+  };
+  uint4 ti[8];
+  float2 ngc;
+  float nbt;
+  auto load_rows = [&](const Item& x) {
+    load_tinv<true>(w.tinvt + x.cb * 32 * 128, r, h, 4 * q, 16, ti);
+    ngc = w.gc[x.cb * kGdnL + r];
+    nbt = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
+  };
 
+  Item x(blockIdx.x, p, w);
   if (tid == 0) {
-    mbar_init(bar_in, 1);
+    mbar_init(bar_qk, 1);
+    mbar_init(bar_h, 1);
     mbar_init(bar, 1);
     fence_barrier_init();
-    mbar_expect_tx(bar_in, (2 * slabs + 1) * kBlk);
-    const int kh = gdn_key_head(p, bh);
-    for (int s = 0; s < slabs; ++s) {
-      tma_load_3d(ka + s * kBlk, &tm_k, s * 64, t0, kh, bar_in);
-      tma_load_3d(qa + s * kBlk, &tm_q, s * 64, t0, kh, bar_in);
-    }
-    tma_load_3d(ia, &tm_dh, vt * 64, t0, bh, bar_in);
+    load_qk(x);
+    load_dh(x);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32((const void*)slot), 256);
+    tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
   }
-  if (h == 0) gc[r] = w.gc[cb * kGdnL + r];
-  const float bt = r < n ? beta[(long)bh * p.T + t0 + r] : 0.f;
+  load_rows(x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-  const float2 gr = gc[r];
-  const float lam = gdn_exp(gr);
-  bool ok = mbar_wait(bar_in, 0, wt, 0x70);
-  uint32_t phase = 0;
-  constexpr uint32_t id = idesc_bf16(128, 64, 0, 1), idt = idesc_bf16(128, 64, 1, 1);
-  uint4 dh[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    dh[e] = *reinterpret_cast<const uint4*>(img + sw128_offset(r, h * 4 + e));
+  const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + h * 32;
+  const uint32_t at = (h >> 1) * kBlk;  // this thread's value tile in an image
+  bool ok = true;
+  uint32_t phase = 0, in_phase = 0;
 
-  run_mma(bar, phase, ok, wt, 0x71, [&] {
-    mma_ss<false, false>(tmem, ka, qa, idesc_bf16(128, 128, 0, 0), slabs, true);
-  });
-  uint32_t v[32];
-  // row s of (Gam . QK^T)^T: queries 64 h .. ; terms take the scores' columns
-  if (h * 64 + 63 >= q * 32) {
-    float x[64];
+  for (long i = blockIdx.x; i < items; i += gridDim.x, in_phase ^= 1) {
+    const bool more = i + gridDim.x < items;
+    const Item nx(more ? i + gridDim.x : i, p, w);
+    const bool cols = h < 2 * x.tiles;
+    const uint32_t id = idesc_bf16(128, x.tiles * 64, 0, 1), idt = idesc_bf16(128, x.tiles * 64, 1, 1);
+    const float2 gr = ngc;
+    const float bt = nbt, lam = gdn_exp(gr), sl = p.scale * lam;
+    if (h == 0) gc[r] = gr;
+    put_tinv(trow + 128, ti);
+    if (more) load_rows(nx);
+    uint4 dh[4];
+    run_mma(
+        bar, phase, ok, wt, 0x71,
+        [&] {
+          ok = mbar_wait(bar_qk, in_phase, wt, 0x70);
+          tc_fence_after();
+          if (ok) mma_ss<false, false>(tmem, ka, qa, idesc_bf16(128, 128, 0, 0), slabs, true);
+        },
+        [&] {
+          if (ok) ok = mbar_wait(bar_h, in_phase, wt, 0x6e);
+          if (!cols) return;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      tmem_ld32(trow + h * 64 + b * 32, v);
-      tmem_wait_ld();
+          for (int cc = 0; cc < 4; ++cc) {
+            dh[cc] = *reinterpret_cast<const uint4*>(smem + kZDh + at +
+                                                     sw128_offset(r, (h & 1) * 4 + cc));
+            float y[8];
+            unpack8(dh[cc], y);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int t = h * 64 + b * 32 + e;
-        x[b * 32 + e] = t >= r ? gdn_decay(gc[t], gr) * __uint_as_float(v[e]) : 0.f;
+            for (int e = 0; e < 8; ++e) y[e] *= sl;
+            put8(smem + kZL + at, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+          }
+        });
+    uint32_t v[32];
+    {  // row s of (Gam . QK^T)^T: 32 queries; terms take the scores' columns
+      uint32_t hi[16], lo[16];
+      if (h >= q) {
+        tmem_ld32(trow, v);
+        tmem_wait_ld();
+        float g[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int t = h * 32 + e;
+          g[e] = t >= r ? gdn_decay(gc[t], gr) * __uint_as_float(v[e]) : 0.f;
+        }
+        split_pack<32>(g, hi, lo);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
       }
+      tmem_st16(trow, hi);
+      tmem_st16(trow + 16, lo);
     }
-    uint32_t hi[32], lo[32];
-    split_pack<64>(x, hi, lo);
-    tmem_st32(trow + h * 64, hi);
-    tmem_st32(trow + h * 64 + 32, lo);
-  } else {
+    run_mma(bar, phase, ok, wt, 0x72, [&] {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = 0u;
-    tmem_st32(trow + h * 64, v);
-    tmem_st32(trow + h * 64 + 32, v);
-  }
-  uint4 ti[16];
-  load_tinv<true>(w.tinvt + cb * 32 * 128, r, h, 4 * q, 16, ti);
-  run_mma(bar, phase, ok, wt, 0x72, [&] {
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(tmem + 256, tmem + (kk >> 1) * 32 + t * 16 + (kk & 1) * 8, mnmaj(ha, kk), id,
+                      (t | kk) != 0);
+      for (int t = 0; t < 2; ++t)
+        mma_ss<true, true>(tmem + 384, qa, la + 2 * t * kBlk, idt, 2, t == 0);
+    });
+    if (tid == 0 && more && ok) load_dh(nx);
+    auto put = [&](float f) {  // f times the 32 columns in v
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_bf16_ts(tmem + 128, tmem + (kk >> 2) * 64 + t * 32 + (kk & 3) * 8, mnmaj(ia, kk), id,
-                    (t | kk) != 0);
-  });
-  put_tinv(trow, h, ti);
-  const float wf = p.scale * bt;
-  auto put = [&](float f) {  // f times the 32 columns in v
+      for (int cc = 0; cc < 4; ++cc) {
+        float y[8];
 #pragma unroll
-    for (int cc = 0; cc < 4; ++cc) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = f * __uint_as_float(v[8 * cc + e]);
-      put8(img, kBlk, r, h * 4 + cc, x);
+        for (int e = 0; e < 8; ++e) y[e] = f * __uint_as_float(v[8 * cc + e]);
+        put8(smem + kZW + at, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+      }
+    };
+    if (cols) {
+      tmem_ld32(trow + 256, v);
+      tmem_wait_ld();
+      put(p.scale * bt);
     }
-  };
-  tmem_ld32(trow + 128 + h * 32, v);
-  tmem_wait_ld();
-  put(wf);
-  run_mma(bar, phase, ok, wt, 0x73, [&] { mma_terms3(tmem + 128, tmem, ia, kBlk, id); });
-  tmem_ld32(trow + 128 + h * 32, v);
-  tmem_wait_ld();
-  const size_t nb = ((cb * w.nvt + vt) * 16 + h * 8) * 128 + r;
-  put_n(w.dz0 + nb, v);
-  put(-lam);
-  run_mma(bar, phase, ok, wt, 0x74, [&] {
-    mma_ss<true, true>(tmem + 192, ka, ia, idt, 2, true);
-    mma_ss<true, true>(tmem + 192, ka, ia + kBlk, idt, 2, false);
-  });
-  const float sl = p.scale * lam;
+    run_mma(
+        bar, phase, ok, wt, 0x73,
+        [&] { mma_terms3(tmem + 256, tmem + 128, wa, 2 * kBlk, id); },
+        [&] {
+          if (!cols) return;
 #pragma unroll
-  for (int cc = 0; cc < 4; ++cc) {
-    float x[8];
-    unpack8(dh[cc], x);
+          for (int cc = 0; cc < 4; ++cc) {
+            float y[8];
+            unpack8(dh[cc], y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= sl;
-    put8(img, kBlk, r, h * 4 + cc, x);
+            for (int e = 0; e < 8; ++e) y[e] = third(y[e] * sl);
+            put8_one(smem + kZL + at, r, (h & 1) * 4 + cc, y);
+          }
+        });
+    const size_t nb = ((x.cb * w.nvt + x.vt + (h >> 1)) * 16 + (h & 1) * 8) * 128 + r;
+    if (cols) {
+      tmem_ld32(trow + 256, v);
+      tmem_wait_ld();
+      put_n(w.dz0 + nb, v);
+      put(-lam);
+    }
+    run_mma(bar, phase, ok, wt, 0x74, [&] {
+      for (int t = 0; t < 2; ++t) mma_ss<true, true>(tmem + 384, ka, wa + 2 * t * kBlk, idt, 2, false);
+      mma_ss<true, true>(tmem + 384, qa, la, idt, 2, false);
+    });
+    if (tid == 0 && more && ok) load_qk(nx);
+    if (cols) {
+      tmem_ld32(trow + 384, v);
+      tmem_wait_ld();
+      put_n(w.N + nb, v);
+    }
+    x = nx;
   }
-  run_mma(bar, phase, ok, wt, 0x75, [&] {
-    mma_ss<true, true>(tmem + 192, qa, ia, idt, 2, false);
-    mma_ss<true, true>(tmem + 192, qa, ia + kBlk, idt, 2, false);
-  });
-#pragma unroll
-  for (int cc = 0; cc < 4; ++cc) {
-    float x[8];
-    unpack8(dh[cc], x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = third(x[e] * sl);
-    put8_one(img, r, h * 4 + cc, x);
-  }
-  run_mma(bar, phase, ok, wt, 0x6f,
-          [&] { mma_ss<true, true>(tmem + 192, qa, ia, idt, 2, false); });
-  tmem_ld32(trow + 192 + h * 32, v);
-  tmem_wait_ld();
-  put_n(w.N + nb, v);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-// ---------------------------------------------------------------- y, dz, dV
-constexpr uint32_t kYBar = 7 * kBlk;
-constexpr uint32_t kYSmem = kYBar + 64;
+// ---------------------------------------------------------------- dz, dV
+// Tensor memory: Tinv^T [0, 128), K dS' [128, 256), dz [256, 384).
+constexpr uint32_t kYDs = 2 * kBlk, kYW = 8 * kBlk, kYBar = 12 * kBlk;
+constexpr uint32_t kYSmem = kYBar + 64 + 1024;
 
-__global__ void __launch_bounds__(kThreads, 2)
-gdn_tc_ydz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
-                  const float* __restrict__ beta, const __nv_bfloat16* __restrict__ V,
-                  __nv_bfloat16* __restrict__ dV, GdnTcWs w) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 1)
+gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
+                 const float* __restrict__ beta, __nv_bfloat16* __restrict__ dV, GdnTcWs w) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  uint8_t *img = smem + 2 * kBlk, *imgd = smem + 4 * kBlk;  // S, z, y; dS', its z, dz
-  const uint32_t ka = sbase, ia = sbase + 2 * kBlk, da = sbase + 4 * kBlk;
+  const uint32_t ka = sbase, da = sbase + kYDs, wa = sbase + kYW;
   const uint32_t bar_in = sbase + kYBar, bar = bar_in + 8;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kYBar + 32);
-  const int vt = blockIdx.x, c = blockIdx.y, bh = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
-  const int t0 = c * kGdnL, n = min(kGdnL, p.T - t0), v0 = vt * 64 + h * 32;
   const int slabs = (p.DK + 63) / 64;
-  const size_t cb = (size_t)bh * w.NC + c, ct = cb * w.nvt + vt,
-               tile = ct * 2 * kBlk;
+  const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
   const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
+  auto load_tiles = [&](const Item& x) {
+    mbar_expect_tx(bar_in, slabs * (kBlk + x.tiles * 3 * 8192));
+    const int kh = gdn_key_head(p, x.bh);
+    for (int s = 0; s < slabs; ++s) tma_load_3d(ka + s * kBlk, &tm_k, s * 64, x.t0, kh, bar_in);
+    for (int v = 0; v < x.tiles; ++v)
+      for (int t = 0; t < 3; ++t)
+        bulk_load(da + (2 * t + v) * kBlk, w.dS + ((x.cb * w.nvt + x.vt + v) * 3 + t) * kBlk,
+                  slabs * 8192, bar_in);
+  };
+  uint4 ti[8];
+  float2 ngc, ngl;
+  float nbt;
+  auto load_rows = [&](const Item& x) {
+    load_tinv<true>(w.tinvt + x.cb * 32 * 128, r, h, 4 * q, 16, ti);
+    ngc = w.gc[x.cb * kGdnL + r];
+    ngl = w.gc[x.cb * kGdnL + kGdnL - 1];
+    nbt = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
+  };
 
+  Item x(blockIdx.x, p, w);
   if (tid == 0) {
     mbar_init(bar_in, 1);
     mbar_init(bar, 1);
     fence_barrier_init();
-    mbar_expect_tx(bar_in, slabs * (kBlk + 5 * 8192));
-    const int kh = gdn_key_head(p, bh);
-    for (int s = 0; s < slabs; ++s) tma_load_3d(ka + s * kBlk, &tm_k, s * 64, t0, kh, bar_in);
-    for (int t = 0; t < 3; ++t) {
-      if (t < 2) bulk_load(ia + t * kBlk, w.S + tile + t * kBlk, slabs * 8192, bar_in);
-      bulk_load(da + t * kBlk, w.dS + (ct * 3 + t) * kBlk, slabs * 8192, bar_in);
-    }
+    load_tiles(x);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32((const void*)slot), 256);
+    tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
   }
-  uint4 ti[16];
-  load_tinv<false>(w.tinv + cb * 32 * 128, r, h, 0, 4 * (q + 1), ti);
-  const size_t vb = ((size_t)bh * p.T + t0 + r) * p.DV + v0;
-  uint4 vrow[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    vrow[e] = r < n && v0 + 8 * e < p.DV ? *reinterpret_cast<const uint4*>(V + vb + 8 * e)
-                                         : make_uint4(0u, 0u, 0u, 0u);
-  const float2 gr = w.gc[cb * kGdnL + r], gl = w.gc[cb * kGdnL + kGdnL - 1];
-  const float bt = r < n ? beta[(long)bh * p.T + t0 + r] : 0.f;
-  const float lam = gdn_exp(gr), dec = gdn_decay(gl, gr);
+  load_rows(x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+  const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + h * 32;
+  uint8_t* img = smem + kYW + (h >> 1) * kBlk;
   bool ok = true;
-  uint32_t phase = 0;
-  constexpr uint32_t id = idesc_bf16(128, 64, 0, 1);
-  put_tinv(trow, h, ti);
-  run_mma(bar, phase, ok, wt, 0x76, [&] {
-    ok = mbar_wait(bar_in, 0, wt, 0x79);
-    tc_fence_after();
-    if (!ok) return;
-    for (int t = 0; t < 3; ++t) {
-      if (t < 2) mma_ss<false, true>(tmem + 128, ka, ia + t * kBlk, id, slabs, t == 0);
-      mma_ss<false, true>(tmem + 192, ka, da + t * kBlk, id, slabs, t == 0);
-    }
-  });
-  uint32_t v[32];
-  tmem_ld32(trow + 192 + h * 32, v);
-  tmem_wait_ld();
+  uint32_t phase = 0, in_phase = 0;
+
+  for (long i = blockIdx.x; i < items; i += gridDim.x) {
+    const bool more = i + gridDim.x < items;
+    const Item nx(more ? i + gridDim.x : i, p, w);
+    const bool cols = h < 2 * x.tiles;
+    const uint32_t id = idesc_bf16(128, x.tiles * 64, 0, 1);
+    const size_t ct = x.cb * w.nvt + x.vt + (h >> 1);
+    const float dec = gdn_decay(ngl, ngc), bd = nbt * dec;
+    put_tinv(trow, ti);
+    if (more) load_rows(nx);
+    uint4 yh[4], yl[4];
+    if (cols) {  // y of this thread's columns, both terms
+      const uint8_t* src = w.y + ct * 2 * kBlk;
 #pragma unroll
-  for (int cc = 0; cc < 4; ++cc) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = bt * dec * __uint_as_float(v[8 * cc + e]);
-    put8(imgd, kBlk, r, h * 4 + cc, x);
-  }
-  float z[32];
-  tmem_ld32(trow + 128 + h * 32, v);
-  tmem_wait_ld();
-#pragma unroll
-  for (int cc = 0; cc < 4; ++cc) {
-    float x[8];
-    unpack8(vrow[cc], x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      z[8 * cc + e] = fmaf(-lam, __uint_as_float(v[8 * cc + e]), x[e]);
-    put8(img, kBlk, r, h * 4 + cc, z + 8 * cc);
-  }
-  load_tinv<true>(w.tinvt + cb * 32 * 128, r, h, 4 * q, 16, ti);
-  run_mma(bar, phase, ok, wt, 0x77, [&] { mma_terms3(tmem + 128, tmem, ia, kBlk, id); });
-  put_tinv(trow, h, ti);
-  {
-    uint32_t xd[32];
-    tmem_ld32(trow + 128 + h * 32, v);
-    tmem_ld32(trow + 192 + h * 32, xd);
-    tmem_wait_ld();
-    float o = 0.f;
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc) {
-#pragma unroll
-      for (int e = 8 * cc; e < 8 * cc + 8; ++e) {
-        z[e] += __uint_as_float(v[e]);
-        o = fmaf(z[e], __uint_as_float(xd[e]), o);
+      for (int cc = 0; cc < 4; ++cc) {
+        const uint32_t off = sw128_offset(r, (h & 1) * 4 + cc);
+        yh[cc] = *reinterpret_cast<const uint4*>(src + off);
+        yl[cc] = *reinterpret_cast<const uint4*>(src + kBlk + off);
       }
-      put8(img, kBlk, r, h * 4 + cc, z + 8 * cc);
     }
-    w.out[ct * 256 + h * 128 + r] = dec * o;
-  }
-  float4 z0[8];
-  const float4* zp = w.dz0 + (ct * 16 + h * 8) * 128 + r;
+    if (tid == 0) tma_store_wait_read_all();  // dz of the item before has left
+    run_mma(bar, phase, ok, wt, 0x76, [&] {
+      ok = mbar_wait(bar_in, in_phase, wt, 0x79);
+      tc_fence_after();
+      if (!ok) return;
+      for (int t = 0; t < 3; ++t)
+        mma_ss<false, true>(tmem + 128, ka, da + 2 * t * kBlk, id, slabs, t == 0);
+    });
+    in_phase ^= 1;
+    if (tid == 0 && more && ok) load_tiles(nx);
+    uint32_t v[32];
+    float4 z0[8];
+    if (cols) {
+      tmem_ld32(trow + 128, v);
+      tmem_wait_ld();
+      float o = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) z0[e] = zp[e * 128];
-  run_mma(bar, phase, ok, wt, 0x78, [&] { mma_terms3(tmem + 192, tmem, da, kBlk, id); });
-  if (tid == 0) {
-    bulk_store(w.y + tile, ia, 2 * kBlk);
-    tma_store_commit();
-  }
-  tmem_ld32(trow + 192 + h * 32, v);
-  tmem_wait_ld();
+      for (int cc = 0; cc < 4; ++cc) {
+        float a[8], b[8];
+        unpack8(yh[cc], a);
+        unpack8(yl[cc], b);
 #pragma unroll
-  for (int cc = 0; cc < 4; ++cc) {
-    const float4 a = z0[2 * cc], b = z0[2 * cc + 1];
-    float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        for (int e = 0; e < 8; ++e) {
+          const float xd = __uint_as_float(v[8 * cc + e]);
+          o = fmaf(a[e] + b[e], xd, o);
+          a[e] = bd * xd;
+        }
+        put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, a);
+      }
+      w.out[ct * 256 + (h & 1) * 128 + r] = dec * o;
+      const float4* zp = w.dz0 + (ct * 16 + (h & 1) * 8) * 128 + r;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += __uint_as_float(v[8 * cc + e]);
-    put8(imgd, kBlk, r, h * 4 + cc, x);
-    if (r < n && ok && v0 + 8 * cc < p.DV) *reinterpret_cast<uint4*>(dV + vb + 8 * cc) = pack8(x);
+      for (int e = 0; e < 8; ++e) z0[e] = zp[e * 128];
+    }
+    run_mma(bar, phase, ok, wt, 0x78, [&] { mma_terms3(tmem + 256, tmem, wa, 2 * kBlk, id); });
+    if (cols) {
+      tmem_ld32(trow + 256, v);
+      tmem_wait_ld();
+      const int v0 = x.vt * 64 + h * 32;
+      __nv_bfloat16* dst = dV + ((size_t)x.bh * p.T + x.t0 + r) * p.DV + v0;
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        const float4 a = z0[2 * cc], b = z0[2 * cc + 1];
+        float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += __uint_as_float(v[8 * cc + e]);
+        put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+        if (r < x.n && ok && v0 + 8 * cc < p.DV)
+          *reinterpret_cast<uint4*>(dst + 8 * cc) = pack8(y);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {  // every thread has read its part of dz0, which dz replaces
+      for (int t = 0; t < x.tiles; ++t)
+        for (int term = 0; term < 2; ++term)
+          bulk_store(w.dz + ((x.cb * w.nvt + x.vt + t) * 2 + term) * kBlk,
+                     wa + (2 * term + t) * kBlk, kBlk);
+      tma_store_commit();
+    }
+    x = nx;
   }
-  fence_proxy_async_smem();
-  tc_fence_before();
+  if (tid == 0) tma_store_wait_all();
   __syncthreads();
-  if (tid == 0) {  // every thread has read its part of dz0, which dz replaces
-    bulk_store(w.dz + tile, da, 2 * kBlk);
-    tma_store_commit();
-    tma_store_wait_all();
-  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -697,22 +760,25 @@ cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const Gdn
       !encode_tmap_bf16_3d(&th, d.dH, p.DV, p.T, p.BH, 64, kGdnL))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(
-      gdn_tc_dz0_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      gdn_tc_dz0_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kZSmem);
   if (e != cudaSuccess) return e;
-  gdn_tc_dz0_kernel<<<dim3(w.nvt, w.NC, p.BH), kThreads, kSmem, st>>>(tq, tk, th, p, x.beta, w);
+  const long n = items_of(p, w);
+  gdn_tc_dz0_kernel<<<(unsigned)(n < kSms ? n : kSms), kThreads, kZSmem, st>>>(tq, tk, th, p, x.beta,
+                                                                              w);
   return cudaGetLastError();
 }
 
-cudaError_t launch_gdn_tc_ydz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
-                              const GdnTcWs& w, cudaStream_t st) {
+cudaError_t launch_gdn_tc_dz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+                             const GdnTcWs& w, cudaStream_t st) {
   CUtensorMap tk;
   if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(
-      gdn_tc_ydz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kYSmem);
+      gdn_tc_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kYSmem);
   if (e != cudaSuccess) return e;
-  gdn_tc_ydz_kernel<<<dim3(w.nvt, w.NC, p.BH), kThreads, kYSmem, st>>>(
-      tk, p, x.beta, static_cast<const __nv_bfloat16*>(x.V), static_cast<__nv_bfloat16*>(d.dV), w);
+  const long n = items_of(p, w);
+  gdn_tc_dz_kernel<<<(unsigned)(n < kSms ? n : kSms), kThreads, kYSmem, st>>>(
+      tk, p, x.beta, static_cast<__nv_bfloat16*>(d.dV), w);
   return cudaGetLastError();
 }
 

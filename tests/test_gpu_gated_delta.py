@@ -95,6 +95,31 @@ def test_gates_and_keys(algo, gates, keys):
     run_case(algo, dict(NHK=1, NH=2, T=333, DK=128, DV=128, gates=gates, keys=keys, seed=7))
 
 
+@pytest.mark.parametrize("size", [(1, 1, 1, 64, 64, 64), (2, 2, 4, 131, 96, 72),
+                                  (1, 1, 2, 300, 128, 256), (1, 2, 2, 513, 128, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("init", [True, False])
+def test_training_pair(size, init):
+    """The pair against fp64; its forward's results are the plain forward's."""
+    B, NHK, NH, T, DK, DV = size
+    x = gd.make(B=B, NHK=NHK, NH=NH, T=T, DK=DK, DV=DV, init=init)
+    d = gd.cuda(x)
+    H, C_T, saved = api.gated_delta_fw_train(*(d[n] for n in gd.NAMES), scale=0.2)
+    H2, C2 = api.gated_delta_fw(*(d[n] for n in gd.NAMES), scale=0.2)
+    assert torch.equal(H, H2) and torch.equal(C_T, C2)
+    gen = torch.Generator().manual_seed(1)
+    dH = torch.randn(x["V"].shape, generator=gen).to(x["V"].dtype)
+    dC = torch.randn(C_T.shape, generator=gen)
+    got = api.gated_delta_bw_saved(*(d[n] for n in gd.NAMES[:5]), saved, dH.cuda(), d["C0"],
+                                   dC.cuda(), scale=0.2)
+    want = ref.gradients(x, dH, dC, 0.2)
+    check("tc", got, {n: w for n, w in want.items() if n in got})
+    # and the recomputing call's
+    again = api.gated_delta_bw(*(d[n] for n in gd.NAMES[:5]), dH.cuda(), d["C0"], dC.cuda(),
+                               scale=0.2)
+    assert all(torch.equal(got[n], again[n]) for n in got)
+
+
 @pytest.mark.parametrize("algo", ALGOS)
 def test_no_initial_state_and_scale(algo):
     run_case(algo, dict(T=150, init=False, DK=128, DV=64), scale=0.37)
@@ -195,8 +220,8 @@ def test_prefill_then_steps():
     check("tc", {"H": torch.cat([H, torch.stack(hs, 2)], 2), "C": C}, {"H": H64, "C": C64})
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_autograd(dtype):
+@pytest.mark.parametrize("dtype,recompute", [("bf16", False), ("bf16", True), ("f32", False)])
+def test_autograd(dtype, recompute):
     """Gradients of losses on H, on C_T and on both, through the public call."""
     x = gd.make(NHK=1, NH=2, T=140, DK=64, DV=64, dtype=dtype)
     gen = torch.Generator().manual_seed(9)
@@ -204,7 +229,7 @@ def test_autograd(dtype):
     wC = torch.randn(x["C0"].shape, generator=gen)
     for use_h, use_c in ((True, False), (False, True), (True, True)):
         d = {n: v.detach().requires_grad_() for n, v in gd.cuda(x).items()}
-        H, C = api.gated_delta_chunkwise(*(d[n] for n in gd.NAMES))
+        H, C = api.gated_delta_chunkwise(*(d[n] for n in gd.NAMES), recompute=recompute)
         # wH carries a stride that the upstream gradient hands on
         up = wH.cuda().transpose(1, 2).contiguous().transpose(1, 2)
         outs, ws = ([H] if use_h else []) + ([C] if use_c else []), \
