@@ -24,26 +24,28 @@ using namespace tc;
 
 constexpr int kThreads = 512;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kBlk, kOffS = 4 * kBlk, kOffZ = 8 * kBlk;
-constexpr uint32_t kOffGc = 12 * kBlk;            // float2[128]
+constexpr uint32_t kOffV = 12 * kBlk;
+constexpr uint32_t kOffGc = 14 * kBlk;            // float2[128]
 constexpr uint32_t kOffBeta = kOffGc + 1024;      // float[128]
-constexpr uint32_t kOffBar = kOffBeta + 512;
-constexpr uint32_t kSmem = kOffBar + 64 + 1024;
+constexpr uint32_t kOffCol = kOffBeta + 512;      // float[128], beta times the column's factor
+constexpr uint32_t kOffBar = kOffCol + 512;
+constexpr uint32_t kSmem = kOffBar + 64;
+static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // kH: writes H.  kY: keeps y for the backward.
 template <bool kH, bool kY>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  GdnProblem p, const float* __restrict__ beta,
-                  const __nv_bfloat16* __restrict__ V, __nv_bfloat16* __restrict__ H, GdnTcWs w) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_h,
+                  GdnProblem p, const float* __restrict__ beta, GdnTcWs w) {
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   float2* gc = reinterpret_cast<float2*>(smem + kOffGc);
   float* sbeta = reinterpret_cast<float*>(smem + kOffBeta);
+  float* scol = reinterpret_cast<float*>(smem + kOffCol);
   uint8_t* img = smem + kOffZ;
   const uint32_t qa = sbase + kOffQ, ka = sbase + kOffK, sa = sbase + kOffS, za = sbase + kOffZ;
-  const uint32_t bar_in = sbase + kOffBar, bar = bar_in + 8;
+  const uint32_t bar_in = sbase + kOffBar, bar = bar_in + 8, bar_v = bar_in + 16;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
@@ -76,15 +78,14 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         bulk_load(sa + (2 * t + v) * kBlk, w.S + ((x.cb * w.nvt + x.vt + v) * 2 + t) * kBlk,
                   slabs * 8192, bar_in);
   };
-  uint4 ti[8], vrow[4];
+  auto load_v = [&](const Item& x) {
+    mbar_expect_tx(bar_v, x.tiles * kBlk);
+    for (int v = 0; v < x.tiles; ++v)
+      tma_load_3d(sbase + kOffV + v * kBlk, &tm_v, (x.vt + v) * 64, x.t0, x.bh, bar_v);
+  };
+  uint4 ti[8];
   auto load_rows = [&](const Item& x) {
-    load_tinv<true>(w.tinv + x.cb * 32 * 128, r, h, 0, 4 * (q + 1), ti);
-    const int v0 = x.vt * 64 + h * 32;
-    const __nv_bfloat16* src = V + ((long)x.bh * p.T + x.t0 + r) * p.DV + v0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      vrow[e] = r < x.n && v0 + 8 * e < p.DV ? *reinterpret_cast<const uint4*>(src + 8 * e)
-                                             : make_uint4(0u, 0u, 0u, 0u);
+    load_tinv(w.tinv + x.cb * 32 * 128, r, h, h <= q, ti);
   };
   auto load_gates = [&](const Item& x, float2& g, float& b) {  // by the first 128 threads
     g = w.gc[x.cb * kGdnL + tid];
@@ -95,8 +96,10 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   if (tid == 0) {
     mbar_init(bar_in, 1);
     mbar_init(bar, 1);
+    mbar_init(bar_v, 1);
     fence_barrier_init();
     load_tiles(x);
+    load_v(x);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32((const void*)slot), 512);
@@ -110,7 +113,7 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + h * 32;
+  const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16), trow = tlane + h * 32;
   bool ok = true;
   uint32_t phase = 0, in_phase = 0;
 
@@ -122,10 +125,13 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (tid < 128) {
       gc[tid] = ng;
       sbeta[tid] = nb;
+      scol[tid] = nb * gdn_col_factor(ng, 31);
       if (more) load_gates(nx, ng, nb);
     }
-    put_tinv(trow, ti);
-    if (kY && tid == 0) tma_store_wait_read_all();  // y of the item before has left
+    add_identity(r, h, ti);
+    put_tinv(tlane, h, ti);
+    if (more) load_rows(nx);
+    if (tid == 0) tma_store_wait_read_all();  // what the image held has left
     run_mma(bar, phase, ok, wt, 0x61, [&] {
       ok = mbar_wait(bar_in, in_phase, wt, 0x60);
       tc_fence_after();
@@ -138,8 +144,9 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           mma_ss<false, true>(tmem + 384, qa, sa + 2 * t * kBlk, id, slabs, t == 0);
       }
     });
-    in_phase ^= 1;
     if (tid == 0 && more && ok) load_tiles(nx);
+    if (ok) ok = mbar_wait(bar_v, in_phase, wt, 0x65);
+    in_phase ^= 1;
     const float2 gr = gc[r];
     const float lam = gdn_exp(gr);
     uint32_t v[32];
@@ -149,16 +156,18 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
         float z[8];
-        unpack8(vrow[cc], z);
+        unpack8(*reinterpret_cast<const uint4*>(smem + kOffV + (h >> 1) * kBlk +
+                                                sw128_offset(r, (h & 1) * 4 + cc)),
+                z);
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = fmaf(-lam, __uint_as_float(v[8 * cc + e]), z[e]);
         put8(img + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc, z);
       }
     }
-    if (more) load_rows(nx);
     run_mma(
         bar, phase, ok, wt, 0x62, [&] { mma_terms3(tmem + 256, tmem, za, 2 * kBlk, id); },
         [&] {
+          if (tid == 0 && more && ok) load_v(nx);
           if (!kH) return;
           // P: 32 keys of the row; its terms take the scores' columns, hi then lo
           uint32_t hi[16], lo[16];
@@ -167,9 +176,17 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             tmem_wait_ld();
             float s[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int k = h * 32 + e;
-              s[e] = k <= r ? gdn_decay(gr, gc[k]) * sbeta[k] * __uint_as_float(v[e]) : 0.f;
+            for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(v[e]);
+            if (h == q) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int k = h * 32 + e;
+                s[e] = e <= lane ? gdn_decay(gr, gc[k]) * sbeta[k] * s[e] : 0.f;
+              }
+            } else {
+              const float f = gdn_decay(gr, gc[h * 32 + 31]);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] *= f * scol[h * 32 + e];
             }
             split_pack<32>(s, hi, lo);
           } else {
@@ -207,25 +224,35 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             mnmaj(za + (t == 2 ? 2 * kBlk : 0u), kk), id, (t | kk) != 0);
           },
           [&] {
-            if (kY && tid == 0) keep_y();
+            if (!kY) return;
+            if (tid == 0) {
+              keep_y();
+              tma_store_wait_read_all();
+            }
+            __syncthreads();  // H takes y's place
           });
       if (cols) {
         uint32_t o[32];
         tmem_ld32(trow + 256, o);
         tmem_ld32(trow + 384, v);
         tmem_wait_ld();
-        const int v0 = x.vt * 64 + h * 32;
-        __nv_bfloat16* hp = H + ((long)x.bh * p.T + x.t0 + r) * p.DV + v0;
-        if (r < x.n && ok)
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            float y[8];
+        for (int cc = 0; cc < 4; ++cc) {
+          float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              y[e] = p.scale *
-                     fmaf(lam, __uint_as_float(v[8 * cc + e]), __uint_as_float(o[8 * cc + e]));
-            if (v0 + 8 * cc < p.DV) *reinterpret_cast<uint4*>(hp + 8 * cc) = pack8(y);
-          }
+          for (int e = 0; e < 8; ++e)
+            y[e] = p.scale *
+                   fmaf(lam, __uint_as_float(v[8 * cc + e]), __uint_as_float(o[8 * cc + e]));
+          *reinterpret_cast<uint4*>(img + (h >> 1) * kBlk +
+                                    sw128_offset(r, (h & 1) * 4 + cc)) = pack8(y);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0 && ok) {  // rows past T and columns past d_v are clipped
+        for (int t = 0; t < x.tiles; ++t)
+          tma_store_3d(&tm_h, za + t * kBlk, (x.vt + t) * 64, x.t0, x.bh);
+        tma_store_commit();
       }
     } else {
       fence_proxy_async_smem();
@@ -234,7 +261,7 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
     x = nx;
   }
-  if (kY && tid == 0) tma_store_wait_all();
+  if (tid == 0) tma_store_wait_all();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -331,10 +358,12 @@ int gdn_tc_launches(const GdnProblem& p, bool backward) {
 
 cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
                               cudaStream_t st) {
-  CUtensorMap tq, tk;
+  CUtensorMap tq, tk, tv, th;
   const uint64_t kheads = (uint64_t)p.B * p.NHK;
   if (!encode_tmap_bf16_3d(&tq, x.Q, p.DK, p.T, kheads, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, kheads, 64, kGdnL))
+      !encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, kheads, 64, kGdnL) ||
+      !encode_tmap_bf16_3d(&tv, x.V, p.DV, p.T, p.BH, 64, kGdnL) ||
+      !encode_tmap_bf16_3d(&th, H ? H : x.V, p.DV, p.T, p.BH, 64, kGdnL))
     return cudaErrorInvalidValue;
   auto kern = !H ? gdn_tc_out_kernel<false, true>
                  : w.y ? gdn_tc_out_kernel<true, true> : gdn_tc_out_kernel<true, false>;
@@ -343,7 +372,7 @@ cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, 
   if (e != cudaSuccess) return e;
   const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
   kern<<<(unsigned)(items < kSms ? items : kSms), kThreads, kSmem, st>>>(
-      tq, tk, p, x.beta, static_cast<const __nv_bfloat16*>(x.V), static_cast<__nv_bfloat16*>(H), w);
+      tq, tk, tv, th, p, x.beta, w);
   return cudaGetLastError();
 }
 

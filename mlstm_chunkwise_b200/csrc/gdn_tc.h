@@ -190,6 +190,16 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Gam of a 32-column block left of the diagonal's is a product of two factors
+// below one, e^{gc_r - gc_m} e^{gc_m - gc_s} with m the block's last token (or,
+// transposed, e^{gc_t - gc_m} e^{gc_m - gc_r} with m its first), so that one
+// exponential per row and one per column replace one per element.
+// Factor of column s, by the thread of token s (a warp holds a block).
+__device__ __forceinline__ float gdn_col_factor(float2 g, int m) {
+  const float2 gm = make_float2(__shfl_sync(0xffffffffu, g.x, m), __shfl_sync(0xffffffffu, g.y, m));
+  return m ? gdn_decay(gm, g) : gdn_decay(g, gm);
+}
+
 // The block as one: everything written so far (shared memory, tensor memory) is
 // visible to the products that `issue` starts, and the block waits for them
 // (and does `meanwhile` before it waits).
@@ -233,35 +243,37 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
 }
 
 // Tinv (or Tinv^T) of row r into tensor memory as the A operand: hi in columns
-// [0, 64), lo in [64, 128).  512 threads: thread h of the row takes pieces
-// 8 (h & 1) .. of term h >> 1 to columns 32 h ...  `from`, `to`: the pieces that
-// exist (the rest is zero).  kOne: with the identity.
-template <bool kOne>
-__device__ __forceinline__ void load_tinv(const uint4* src, int r, int h, int from, int to,
+// [0, 64), lo in [64, 128).  512 threads: thread h of the row takes both terms of
+// columns 32 h ..: pieces 4 h .. 4 h + 3, t[0..3] hi and t[4..7] lo.  `have`: the
+// row has them (else zero).  The identity is added on the way into tensor memory,
+// not to the loads, which would wait for them.
+__device__ __forceinline__ void load_tinv(const uint4* src, int r, int h, bool have,
                                           uint4 (&t)[8]) {
-  const uint32_t one = kOne && h < 2 ? 0x3f80u << (16 * (r & 1)) : 0u;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = (h & 1) * 8 + k;
-    t[k] = i >= from && i < to ? src[((h >> 1) * 16 + i) * 128 + r] : make_uint4(0u, 0u, 0u, 0u);
-    if (kOne && i == r >> 3) {
+  for (int k = 0; k < 8; ++k)
+    t[k] = have ? src[((k >> 2) * 16 + h * 4 + (k & 3)) * 128 + r] : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void add_identity(int r, int h, uint4 (&t)[8]) {
+  const uint32_t one = 0x3f80u << (16 * (r & 1));
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (h * 4 + k == r >> 3) {
       const int e = (r >> 1) & 3;
       t[k].x |= e == 0 ? one : 0u;
       t[k].y |= e == 1 ? one : 0u;
       t[k].z |= e == 2 ? one : 0u;
       t[k].w |= e == 3 ? one : 0u;
     }
-  }
 }
-// trow: the thread's lane and first column.
-__device__ __forceinline__ void put_tinv(uint32_t trow, const uint4 (&t)[8]) {
+// tlane: the thread's lane, first column of the operand.
+__device__ __forceinline__ void put_tinv(uint32_t tlane, int h, const uint4 (&t)[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t v[16] = {t[4 * i].x,     t[4 * i].y,     t[4 * i].z,     t[4 * i].w,
                             t[4 * i + 1].x, t[4 * i + 1].y, t[4 * i + 1].z, t[4 * i + 1].w,
                             t[4 * i + 2].x, t[4 * i + 2].y, t[4 * i + 2].z, t[4 * i + 2].w,
                             t[4 * i + 3].x, t[4 * i + 3].y, t[4 * i + 3].z, t[4 * i + 3].w};
-    tmem_st16(trow + i * 16, v);
+    tmem_st16(tlane + i * 64 + h * 16, v);
   }
 }
 // D = A B: A in tensor memory at `a` (hi, lo 64 columns behind), 128 inner

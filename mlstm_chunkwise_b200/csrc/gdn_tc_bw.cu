@@ -44,8 +44,9 @@ inline long items_of(const GdnProblem& p, const GdnTcWs& w) {
 // terms: two go under the first round, the third under the third.
 constexpr uint32_t kZDh = 4 * kBlk, kZL = 6 * kBlk, kZW = 10 * kBlk;
 constexpr uint32_t kZGc = 14 * kBlk;
-constexpr uint32_t kZBar = kZGc + 1024;
-constexpr uint32_t kZSmem = kZBar + 64 + 1024;
+constexpr uint32_t kZCol = kZGc + 1024;  // float[128]: the columns' factors
+constexpr uint32_t kZBar = kZCol + 512;
+constexpr uint32_t kZSmem = kZBar + 64;
 static_assert(kZSmem <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ void put_n(float4* dst, const uint32_t (&v)[32]) {
@@ -59,11 +60,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_dh, GdnProblem p,
                   const float* __restrict__ beta, GdnTcWs w) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   float2* gc = reinterpret_cast<float2*>(smem + kZGc);
+  float* scol = reinterpret_cast<float*>(smem + kZCol);
   const uint32_t qa = sbase, ka = sbase + 2 * kBlk, ha = sbase + kZDh, la = sbase + kZL,
                  wa = sbase + kZW;
   const uint32_t bar_qk = sbase + kZBar, bar_h = bar_qk + 8, bar = bar_qk + 16;
@@ -90,7 +90,7 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   float2 ngc;
   float nbt;
   auto load_rows = [&](const Item& x) {
-    load_tinv<true>(w.tinvt + x.cb * 32 * 128, r, h, 4 * q, 16, ti);
+    load_tinv(w.tinvt + x.cb * 32 * 128, r, h, h >= q, ti);
     ngc = w.gc[x.cb * kGdnL + r];
     nbt = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
   };
@@ -113,7 +113,7 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + h * 32;
+  const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16), trow = tlane + h * 32;
   const uint32_t at = (h >> 1) * kBlk;  // this thread's value tile in an image
   bool ok = true;
   uint32_t phase = 0, in_phase = 0;
@@ -125,8 +125,12 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t id = idesc_bf16(128, x.tiles * 64, 0, 1), idt = idesc_bf16(128, x.tiles * 64, 1, 1);
     const float2 gr = ngc;
     const float bt = nbt, lam = gdn_exp(gr), sl = p.scale * lam;
-    if (h == 0) gc[r] = gr;
-    put_tinv(trow + 128, ti);
+    if (h == 0) {
+      gc[r] = gr;
+      scol[r] = gdn_col_factor(gr, 0);
+    }
+    add_identity(r, h, ti);
+    put_tinv(tlane + 128, h, ti);
     if (more) load_rows(nx);
     uint4 dh[4];
     run_mma(
@@ -158,9 +162,15 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tmem_wait_ld();
         float g[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int t = h * 32 + e;
-          g[e] = t >= r ? gdn_decay(gc[t], gr) * __uint_as_float(v[e]) : 0.f;
+        for (int e = 0; e < 32; ++e) g[e] = __uint_as_float(v[e]);
+        if (h == q) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            g[e] = e >= lane ? gdn_decay(gc[h * 32 + e], gr) * g[e] : 0.f;
+        } else {
+          const float f = gdn_decay(gc[h * 32], gr);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) g[e] *= f * scol[h * 32 + e];
         }
         split_pack<32>(g, hi, lo);
       } else {
@@ -238,15 +248,14 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
 // ---------------------------------------------------------------- dz, dV
 // Tensor memory: Tinv^T [0, 128), K dS' [128, 256), dz [256, 384).
-constexpr uint32_t kYDs = 2 * kBlk, kYW = 8 * kBlk, kYBar = 12 * kBlk;
-constexpr uint32_t kYSmem = kYBar + 64 + 1024;
+constexpr uint32_t kYDs = 2 * kBlk, kYW = 8 * kBlk, kYDv = 12 * kBlk, kYBar = 14 * kBlk;
+constexpr uint32_t kYSmem = kYBar + 64;
 
 __global__ void __launch_bounds__(kThreads, 1)
-gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
-                 const float* __restrict__ beta, __nv_bfloat16* __restrict__ dV, GdnTcWs w) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_dv, GdnProblem p,
+                 const float* __restrict__ beta, GdnTcWs w) {
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const uint32_t ka = sbase, da = sbase + kYDs, wa = sbase + kYW;
   const uint32_t bar_in = sbase + kYBar, bar = bar_in + 8;
@@ -269,7 +278,7 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
   float2 ngc, ngl;
   float nbt;
   auto load_rows = [&](const Item& x) {
-    load_tinv<true>(w.tinvt + x.cb * 32 * 128, r, h, 4 * q, 16, ti);
+    load_tinv(w.tinvt + x.cb * 32 * 128, r, h, h >= q, ti);
     ngc = w.gc[x.cb * kGdnL + r];
     ngl = w.gc[x.cb * kGdnL + kGdnL - 1];
     nbt = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
@@ -291,7 +300,7 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + h * 32;
+  const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16), trow = tlane + h * 32;
   uint8_t* img = smem + kYW + (h >> 1) * kBlk;
   bool ok = true;
   uint32_t phase = 0, in_phase = 0;
@@ -303,7 +312,8 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
     const uint32_t id = idesc_bf16(128, x.tiles * 64, 0, 1);
     const size_t ct = x.cb * w.nvt + x.vt + (h >> 1);
     const float dec = gdn_decay(ngl, ngc), bd = nbt * dec;
-    put_tinv(trow, ti);
+    add_identity(r, h, ti);
+    put_tinv(tlane, h, ti);
     if (more) load_rows(nx);
     uint4 yh[4], yl[4];
     if (cols) {  // y of this thread's columns, both terms
@@ -353,8 +363,6 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
     if (cols) {
       tmem_ld32(trow + 256, v);
       tmem_wait_ld();
-      const int v0 = x.vt * 64 + h * 32;
-      __nv_bfloat16* dst = dV + ((size_t)x.bh * p.T + x.t0 + r) * p.DV + v0;
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
         const float4 a = z0[2 * cc], b = z0[2 * cc + 1];
@@ -362,8 +370,8 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] += __uint_as_float(v[8 * cc + e]);
         put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, y);
-        if (r < x.n && ok && v0 + 8 * cc < p.DV)
-          *reinterpret_cast<uint4*>(dst + 8 * cc) = pack8(y);
+        *reinterpret_cast<uint4*>(smem + kYDv + (h >> 1) * kBlk +
+                                  sw128_offset(r, (h & 1) * 4 + cc)) = pack8(y);
       }
     }
     fence_proxy_async_smem();
@@ -374,6 +382,9 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
         for (int term = 0; term < 2; ++term)
           bulk_store(w.dz + ((x.cb * w.nvt + x.vt + t) * 2 + term) * kBlk,
                      wa + (2 * term + t) * kBlk, kBlk);
+      if (ok)  // rows past T and columns past d_v are clipped
+        for (int t = 0; t < x.tiles; ++t)
+          tma_store_3d(&tm_dv, sbase + kYDv + t * kBlk, (x.vt + t) * 64, x.t0, x.bh);
       tma_store_commit();
     }
     x = nx;
@@ -770,15 +781,16 @@ cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const Gdn
 
 cudaError_t launch_gdn_tc_dz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
                              const GdnTcWs& w, cudaStream_t st) {
-  CUtensorMap tk;
-  if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL))
+  CUtensorMap tk, tv;
+  if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL) ||
+      !encode_tmap_bf16_3d(&tv, d.dV, p.DV, p.T, p.BH, 64, kGdnL))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(
       gdn_tc_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kYSmem);
   if (e != cudaSuccess) return e;
   const long n = items_of(p, w);
   gdn_tc_dz_kernel<<<(unsigned)(n < kSms ? n : kSms), kThreads, kYSmem, st>>>(
-      tk, p, x.beta, static_cast<__nv_bfloat16*>(d.dV), w);
+      tk, tv, p, x.beta, w);
   return cudaGetLastError();
 }
 

@@ -443,7 +443,7 @@ cudaError_t bw(const HeadNormProblem& p, const Shape& s, const void* X, const vo
   const dim3 grid(blocks, p.NH);
   const size_t ring = kVec > 1 ? (size_t)kBwStages<kNV> * kNV * 32 * s.threads : 0;
   const size_t sums = s.block_row ? 0 : 8 * (size_t)p.D;  // reuses the ring
-  const size_t smem = ring > sums ? ring : sums;
+  const size_t smem = sums > ring ? sums : ring;
   auto kern = s.block_row ? head_norm_bw_kernel<T, kVec, kNV, true>
                           : head_norm_bw_kernel<T, kVec, kNV, false>;
   cudaError_t e = cudaSuccess;
