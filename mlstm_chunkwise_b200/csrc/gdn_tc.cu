@@ -3,11 +3,10 @@
 // Per (bh, chunk, up to 128 value columns), from the state S entering the chunk:
 //   X = K S,  z = V - Lam X,  y = Tinv z,  H = scale (Lam Q S + P y),
 //   P_rs = Gam_rs beta_s q_r.k_s (s <= r)
-// Persistent, one block of 512 threads per SM, thread (r, h) on columns 32 h ..
-// of row r.  Three rounds of products with a pass through registers after each:
+// Persistent, one block per SM.  Three rounds of products with a pass through registers after each:
 // {K S, Q S, Q K^T}, {Tinv z} under which P is formed, {P y}.  The next item's
-// tiles are copied in as soon as the first round has read this one's, and its
-// Tinv and V wait in registers.  88 products of 128 x 128 x 16 (about 6000
+// tiles are copied in as soon as this one's have been read, and its Tinv waits in
+// registers.  88 products of 128 x 128 x 16 (about 6000
 // cycles) per 128 tokens and 240 KB of traffic; two blocks per SM on 64 columns
 // each with four rounds took three times as long (Tinv, Q, K and P twice, loads
 // exposed).
@@ -22,7 +21,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kBlk, kOffS = 4 * kBlk, kOffZ = 8 * kBlk;
 constexpr uint32_t kOffV = 12 * kBlk;
 constexpr uint32_t kOffGc = 14 * kBlk;            // float2[128]
@@ -34,7 +32,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // kH: writes H.  kY: keeps y for the backward.
 template <bool kH, bool kY>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kGdnThreads, 1)
 gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_h,
                   GdnProblem p, const float* __restrict__ beta, GdnTcWs w) {
@@ -43,30 +41,16 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   float2* gc = reinterpret_cast<float2*>(smem + kOffGc);
   float* sbeta = reinterpret_cast<float*>(smem + kOffBeta);
   float* scol = reinterpret_cast<float*>(smem + kOffCol);
-  uint8_t* img = smem + kOffZ;
   const uint32_t qa = sbase + kOffQ, ka = sbase + kOffK, sa = sbase + kOffS, za = sbase + kOffZ;
-  const uint32_t bar_in = sbase + kOffBar, bar = bar_in + 8, bar_v = bar_in + 16;
+  const uint32_t bar_in = sbase + kOffBar, bar_v = bar_in + 8;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
-  const int slabs = (p.DK + 63) / 64, pairs = (w.nvt + 1) / 2;
-  const long items = (long)p.BH * w.NC * pairs;
-  const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
-  struct Item {
-    size_t cb;
-    int bh, t0, n, vt, tiles;
-  };
-  auto item = [&](long i) {
-    Item x;
-    x.cb = (size_t)(i / pairs);
-    x.vt = (int)(i % pairs) * 2;
-    x.tiles = min(2, w.nvt - x.vt);
-    x.bh = (int)(x.cb / w.NC);
-    x.t0 = (int)(x.cb % w.NC) * kGdnL;
-    x.n = min(kGdnL, p.T - x.t0);
-    return x;
-  };
-  auto load_tiles = [&](const Item& x) {
+  const bool row = tid < kGdnRows, lead = tid == kGdnRows;
+  const int slabs = (p.DK + 63) / 64;
+  const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
+  GdnRounds rd{bar_in + 16, 0u, true, Problem{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls}};
+  auto load_tiles = [&](const GdnItem& x) {
     mbar_expect_tx(bar_in, slabs * ((kH ? 2 : 1) * kBlk + x.tiles * 2 * 8192));
     const int kh = gdn_key_head(p, x.bh);
     for (int s = 0; s < slabs; ++s) {
@@ -78,76 +62,81 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         bulk_load(sa + (2 * t + v) * kBlk, w.S + ((x.cb * w.nvt + x.vt + v) * 2 + t) * kBlk,
                   slabs * 8192, bar_in);
   };
-  auto load_v = [&](const Item& x) {
+  auto load_v = [&](const GdnItem& x) {
     mbar_expect_tx(bar_v, x.tiles * kBlk);
     for (int v = 0; v < x.tiles; ++v)
       tma_load_3d(sbase + kOffV + v * kBlk, &tm_v, (x.vt + v) * 64, x.t0, x.bh, bar_v);
   };
   uint4 ti[8];
-  auto load_rows = [&](const Item& x) {
+  float2 ng;
+  float nb;
+  auto load_rows = [&](const GdnItem& x) {
     load_tinv(w.tinv + x.cb * 32 * 128, r, h, h <= q, ti);
-  };
-  auto load_gates = [&](const Item& x, float2& g, float& b) {  // by the first 128 threads
-    g = w.gc[x.cb * kGdnL + tid];
-    b = tid < x.n ? beta[(long)x.bh * p.T + x.t0 + tid] : 0.f;
+    ng = w.gc[x.cb * kGdnL + r];
+    nb = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
   };
 
-  Item x = item(blockIdx.x);
-  if (tid == 0) {
-    mbar_init(bar_in, 1);
-    mbar_init(bar, 1);
-    mbar_init(bar_v, 1);
+  GdnItem x(blockIdx.x, p, w);
+  if (lead) {
+    for (int i = 0; i < 3; ++i) mbar_init(bar_in + 8 * i, 1);
     fence_barrier_init();
     load_tiles(x);
     load_v(x);
   }
-  if (warp == 1) {
+  if (!row) {
+    __syncwarp();
     tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
+  } else {
+    load_rows(x);
   }
-  float2 ng = make_float2(0.f, 0.f);
-  float nb = 0.f;
-  if (tid < 128) load_gates(x, ng, nb);
-  load_rows(x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
   const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16), trow = tlane + h * 32;
-  bool ok = true;
-  uint32_t phase = 0, in_phase = 0;
+  uint8_t* img = smem + kOffZ + (h >> 1) * kBlk;
+  uint32_t in_phase = 0;
 
-  for (long i = blockIdx.x; i < items; i += gridDim.x) {
+  for (long i = blockIdx.x; i < items; i += gridDim.x, in_phase ^= 1) {
     const bool more = i + gridDim.x < items;
-    const Item nx = item(more ? i + gridDim.x : i);
-    const bool cols = h < 2 * x.tiles;  // this thread's value columns exist
+    const GdnItem nx(more ? i + gridDim.x : i, p, w);
+    const bool cols = row && h < 2 * x.tiles;  // this thread's value columns exist
     const uint32_t id = idesc_bf16(128, x.tiles * 64, 0, 1);
-    if (tid < 128) {
-      gc[tid] = ng;
-      sbeta[tid] = nb;
-      scol[tid] = nb * gdn_col_factor(ng, 31);
-      if (more) load_gates(nx, ng, nb);
-    }
-    add_identity(r, h, ti);
-    put_tinv(tlane, h, ti);
-    if (more) load_rows(nx);
-    if (tid == 0) tma_store_wait_read_all();  // what the image held has left
-    run_mma(bar, phase, ok, wt, 0x61, [&] {
-      ok = mbar_wait(bar_in, in_phase, wt, 0x60);
-      tc_fence_after();
-      if (!ok) return;
-      for (int t = 0; t < 2; ++t)
-        mma_ss<false, true>(tmem + 256, ka, sa + 2 * t * kBlk, id, slabs, t == 0);
-      if (kH) {
-        mma_ss<false, false>(tmem + 128, qa, ka, idesc_bf16(128, 128, 0, 0), slabs, true);
-        for (int t = 0; t < 2; ++t)
-          mma_ss<false, true>(tmem + 384, qa, sa + 2 * t * kBlk, id, slabs, t == 0);
+    float2 gr = make_float2(0.f, 0.f);
+    if (row) {
+      gr = ng;
+      if (kH && h == 0) {
+        gc[r] = gr;
+        sbeta[r] = nb;
+        scol[r] = nb * gdn_col_factor(gr, 31);
       }
-    });
-    if (tid == 0 && more && ok) load_tiles(nx);
-    if (ok) ok = mbar_wait(bar_v, in_phase, wt, 0x65);
-    in_phase ^= 1;
-    const float2 gr = gc[r];
+      add_identity(r, h, ti);
+      put_tinv(tlane, h, ti);
+      if (more) load_rows(nx);
+    }
+    if (lead) tma_store_wait_read_all();  // what the image held has left
+    gdn_round(
+        rd, 0x61,
+        [&] {
+          rd.ok = mbar_wait(bar_in, in_phase, rd.wt, 0x60);
+          tc_fence_after();
+          if (!rd.ok) return;
+          for (int t = 0; t < 2; ++t)
+            mma_ss<false, true>(tmem + 256, ka, sa + 2 * t * kBlk, id, slabs, t == 0);
+          if (kH) {
+            mma_ss<false, false>(tmem + 128, qa, ka, idesc_bf16(128, 128, 0, 0), slabs, true);
+            for (int t = 0; t < 2; ++t)
+              mma_ss<false, true>(tmem + 384, qa, sa + 2 * t * kBlk, id, slabs, t == 0);
+          }
+        },
+        [&] {
+          if (rd.ok) rd.ok = mbar_wait(bar_v, in_phase, rd.wt, 0x65);
+        },
+        gdn_nothing,
+        [&] {
+          if (more) load_tiles(nx);
+        });
     const float lam = gdn_exp(gr);
     uint32_t v[32];
     if (cols) {
@@ -161,13 +150,12 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 z);
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = fmaf(-lam, __uint_as_float(v[8 * cc + e]), z[e]);
-        put8(img + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc, z);
+        put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, z);
       }
     }
-    run_mma(
-        bar, phase, ok, wt, 0x62, [&] { mma_terms3(tmem + 256, tmem, za, 2 * kBlk, id); },
+    gdn_round(
+        rd, 0x62, [&] { mma_terms3(tmem + 256, tmem, za, 2 * kBlk, id); },
         [&] {
-          if (tid == 0 && more && ok) load_v(nx);
           if (!kH) return;
           // P: 32 keys of the row; its terms take the scores' columns, hi then lo
           uint32_t hi[16], lo[16];
@@ -195,14 +183,17 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
           tmem_st16(trow + 128, hi);
           tmem_st16(trow + 144, lo);
-        });
+        },
+        [&] {
+          if (more) load_v(nx);
+        },
+        gdn_nothing);
     if (cols) {
       tmem_ld32(trow + 256, v);
       tmem_wait_ld();
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc)
-        put8(img + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc,
-             reinterpret_cast<const float*>(v) + 8 * cc);
+        put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
     }
     auto keep_y = [&] {
       for (int t = 0; t < x.tiles; ++t)
@@ -212,8 +203,8 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       tma_store_commit();
     };
     if (kH) {
-      run_mma(
-          bar, phase, ok, wt, 0x64,
+      gdn_round(
+          rd, 0x64,
           [&] {
 #pragma unroll
             for (int t = 0; t < 3; ++t)
@@ -223,14 +214,14 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             tmem + 128 + (kk >> 1) * 32 + (t == 1 ? 16 : 0) + (kk & 1) * 8,
                             mnmaj(za + (t == 2 ? 2 * kBlk : 0u), kk), id, (t | kk) != 0);
           },
+          gdn_nothing,
           [&] {
             if (!kY) return;
-            if (tid == 0) {
-              keep_y();
-              tma_store_wait_read_all();
-            }
-            __syncthreads();  // H takes y's place
-          });
+            keep_y();
+            tma_store_wait_read_all();
+          },
+          gdn_nothing);
+      if (kY) __syncthreads();  // y has left: H takes its place
       if (cols) {
         uint32_t o[32];
         tmem_ld32(trow + 256, o);
@@ -243,34 +234,31 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int e = 0; e < 8; ++e)
             y[e] = p.scale *
                    fmaf(lam, __uint_as_float(v[8 * cc + e]), __uint_as_float(o[8 * cc + e]));
-          *reinterpret_cast<uint4*>(img + (h >> 1) * kBlk +
-                                    sw128_offset(r, (h & 1) * 4 + cc)) = pack8(y);
+          *reinterpret_cast<uint4*>(img + sw128_offset(r, (h & 1) * 4 + cc)) = pack8(y);
         }
       }
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0 && ok) {  // rows past T and columns past d_v are clipped
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (lead && rd.ok) {
+      if (kH) {  // rows past T and columns past d_v are clipped
         for (int t = 0; t < x.tiles; ++t)
           tma_store_3d(&tm_h, za + t * kBlk, (x.vt + t) * 64, x.t0, x.bh);
         tma_store_commit();
+      } else {
+        keep_y();
       }
-    } else {
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0) keep_y();
     }
     x = nx;
   }
-  if (tid == 0) tma_store_wait_all();
+  if (lead) tma_store_wait_all();
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (!row) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
-
-constexpr long kSms = 148;
 
 constexpr size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -319,8 +307,9 @@ constexpr int kBwParts = kState | kKeep | kInverse | kN | kGrad;
 
 cudaError_t forward(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T, const GdnTcWs& w,
                     cudaStream_t st) {
-  cudaError_t e = launch_gdn_tc_prep(p, x, w, w.tinvt != nullptr, st);
+  cudaError_t e = launch_gdn_tc_inverse(p, x, w, st);
   if (e != cudaSuccess) return e;
+  if ((e = launch_gdn_tc_mn(p, x, w, st)) != cudaSuccess) return e;
   if ((e = launch_gdn_tc_chain(p, false, x.C0, C_T, w, st)) != cudaSuccess) return e;
   return launch_gdn_tc_out(p, x, H, w, st);
 }
@@ -350,10 +339,10 @@ GdnTrainSizes gdn_tc_train_sizes(const GdnProblem& p) {
 }
 
 int gdn_tc_train_launches(const GdnProblem& p, bool backward) {
-  return backward ? 4 + (p.group > 1) : 3;
+  return backward ? 4 + (p.group > 1) : 4;
 }
 int gdn_tc_launches(const GdnProblem& p, bool backward) {
-  return backward ? 3 + gdn_tc_train_launches(p, true) : 3;
+  return backward ? 4 + gdn_tc_train_launches(p, true) : 4;
 }
 
 cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
@@ -370,8 +359,7 @@ cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, 
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
-  kern<<<(unsigned)(items < kSms ? items : kSms), kThreads, kSmem, st>>>(
+  kern<<<gdn_blocks(p, w), kGdnThreads, kSmem, st>>>(
       tq, tk, tv, th, p, x.beta, w);
   return cudaGetLastError();
 }

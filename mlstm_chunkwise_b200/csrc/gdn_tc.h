@@ -81,9 +81,21 @@ cudaError_t launch_gdn_tc_fw_train(const GdnProblem& p, const GdnInputs& x, void
 cudaError_t launch_gdn_tc_bw_saved(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
                                    const void* saved, void* ws, cudaStream_t st);
 
+constexpr long kGdnSms = 148;
+// Items of the persistent kernels, and their blocks.
+inline long gdn_items(const GdnProblem& p, const GdnTcWs& w) {
+  return (long)p.BH * w.NC * ((w.nvt + 1) / 2);
+}
+inline unsigned gdn_blocks(const GdnProblem& p, const GdnTcWs& w) {
+  const long n = gdn_items(p, w);
+  return (unsigned)(n < kGdnSms ? n : kGdnSms);
+}
+
 // The stages, one launch each.
-cudaError_t launch_gdn_tc_prep(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
-                               bool transposed, cudaStream_t st);
+cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
+                                  cudaStream_t st);
+cudaError_t launch_gdn_tc_mn(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
+                             cudaStream_t st);
 // reverse: the gradient's recurrence, from dC_T (init) to dC0 (fin).
 cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* init, float* fin,
                                 const GdnTcWs& w, cudaStream_t st);
@@ -155,6 +167,14 @@ __device__ __forceinline__ void put8_one(uint8_t* img, int r, int c, const float
       make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                  pack_bf16x2(x[6], x[7]));
 }
+// Eight values as a piece of three terms, `term` bytes apart.
+__device__ __forceinline__ void put8x3(uint8_t* img, uint32_t term, int r, int c, const float* x) {
+  put8(img, term, r, c, x);
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = third(x[e]);
+  put8_one(img + 2 * term, r, c, y);
+}
 // Eight bf16 values of a row.
 __device__ __forceinline__ void unpack8(uint4 u, float* x) {
   const uint32_t v[4] = {u.x, u.y, u.z, u.w};
@@ -200,13 +220,71 @@ __device__ __forceinline__ float gdn_col_factor(float2 g, int m) {
   return m ? gdn_decay(gm, g) : gdn_decay(g, gm);
 }
 
-// The block as one: everything written so far (shared memory, tensor memory) is
-// visible to the products that `issue` starts, and the block waits for them
-// (and does `meanwhile` before it waits).
-template <class F, class G>
+// Persistent kernels of 16 row warps, thread (r, h) on columns 32 h .. of row r,
+// and a control warp, which issues the products and moves the tiles: done by a
+// row warp those cost its rows 1500 cycles a round.
+constexpr int kGdnRows = 512;
+constexpr int kGdnThreads = kGdnRows + 32;
+
+struct GdnRounds {
+  uint32_t bar, phase;
+  bool ok;
+  Problem wt;
+};
+
+// One round of the block: everything written so far (shared memory, tensor
+// memory) is visible to the products that `issue` starts.  Meanwhile the row
+// warps run `rows`, and lane 0 of the control warp `moves`; everyone waits for
+// the products, then lane 0 runs `after` (loads into what they have read).
+template <class F, class R, class M, class A>
+__device__ __forceinline__ void gdn_round(GdnRounds& s, uint32_t site, F&& issue, R&& rows,
+                                          M&& moves, A&& after) {
+  fence_proxy_async_smem();
+  tmem_wait_st();
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x >= kGdnRows) {
+    if (elect_one()) {
+      tc_fence_after();
+      if (s.ok) issue();
+      mma_commit(s.bar);
+    }
+    __syncwarp();
+    if (threadIdx.x == kGdnRows) {
+      moves();
+      if (s.ok) s.ok = mbar_wait(s.bar, s.phase, s.wt, site);
+      if (s.ok) after();
+    }
+    __syncwarp();
+  } else {
+    rows();
+    if (s.ok) s.ok = mbar_wait(s.bar, s.phase, s.wt, site);
+    tc_fence_after();
+  }
+  s.phase ^= 1;
+}
+__device__ __forceinline__ void gdn_nothing() {}
+
+// Item i of a persistent kernel: (bh, chunk, pair of value tiles).
+struct GdnItem {
+  size_t cb;
+  int bh, t0, n, vt, tiles;
+  __device__ GdnItem(long i, const GdnProblem& p, const GdnTcWs& w) {
+    const int pairs = (w.nvt + 1) / 2;  // each item has 160 KB of workspace or more: an int holds them
+    const int k = (int)i, c = k / pairs;
+    cb = (size_t)c;
+    vt = (k - c * pairs) * 2;
+    tiles = min(2, w.nvt - vt);
+    bh = c / w.NC;
+    t0 = (c - bh * w.NC) * kGdnL;
+    n = min(kGdnL, p.T - t0);
+  }
+};
+
+// The block as one, without a control warp: thread 0's warp issues.
+template <class F>
 __device__ __forceinline__ void run_mma(uint32_t bar, uint32_t& phase, bool& ok,
-                                        const Problem& wt, uint32_t site, F&& issue,
-                                        G&& meanwhile) {
+                                        const Problem& wt, uint32_t site, F&& issue) {
   fence_proxy_async_smem();
   tmem_wait_st();
   tc_fence_before();
@@ -217,15 +295,9 @@ __device__ __forceinline__ void run_mma(uint32_t bar, uint32_t& phase, bool& ok,
     mma_commit(bar);
   }
   __syncwarp();
-  meanwhile();
   if (ok) ok = mbar_wait(bar, phase, wt, site);
   phase ^= 1;
   tc_fence_after();
-}
-template <class F>
-__device__ __forceinline__ void run_mma(uint32_t bar, uint32_t& phase, bool& ok,
-                                        const Problem& wt, uint32_t site, F&& issue) {
-  run_mma(bar, phase, ok, wt, site, issue, [] {});
 }
 
 // D (+)= A B over an inner axis of 64 * slabs, both operands in shared memory.

@@ -1,17 +1,6 @@
 // Gated delta rule, tensor cores: what a chunk contributes before the state that
-// enters it is known.  Per (bh, chunk): the sums of g, Tinv = (I + A)^{-1} with
-// A_rs = Gam_rs beta_s k_r.k_s (s < r), and M and N of the state recurrence.
-//
-// The inverse goes by blocks.  The four 32 x 32 diagonal blocks by forward
-// substitution in fp32 (a warp per block, a lane per column); then
-// T21 = -T22 A21 T11 for the two 64-blocks at once and for the whole, on the
-// tensor cores with both operands as two bf16 terms (A21 and T22 in tensor
-// memory, T11 and A21 T11 as images).  Every element of A is formed where it is
-// used, from K K^T in tensor memory.
-//
-// About 11 products of 128^3 per chunk and a dozen dependent passes between
-// tensor memory, registers and shared memory: bound by the latency of those
-// passes, so two blocks share an SM (96 KB, 256 tensor-memory columns each).
+// enters it is known: the sums of g and Tinv = (I + A)^{-1} with
+// A_rs = Gam_rs beta_s k_r.k_s (s < r), then M and N of the state recurrence.
 #include <cuda.h>
 
 #include "gdn_tc.h"
@@ -21,33 +10,38 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 256;
-constexpr uint32_t kOffK = 0;             // 2 blocks
-constexpr uint32_t kOffR = 32768;         // 4 blocks: [term][block]
-constexpr uint32_t kOffDiag = kOffR + kBlk;  // float[4][32][kLd], while inverting
-constexpr uint32_t kOffGc = kOffR + 4 * kBlk;
-constexpr uint32_t kOffBeta = kOffGc + 1024;
-constexpr uint32_t kOffLam = kOffBeta + 512;
-constexpr uint32_t kOffBar = kOffLam + 512;
-constexpr uint32_t kSmem = kOffBar + 64 + 1024;
-constexpr int kLd = 36;       // floats per row of a diagonal block
-constexpr uint32_t kBi = 8192;  // lo term of the inversion's images (64 rows)
+// ------------------------------------------------------------------ inverse
+// One block of 256 threads per (bh, chunk), thread (r, h) on one of two column
+// halves of row r.  The inverse goes by blocks: the four 32 x 32 diagonal blocks
+// by forward substitution in fp32 (a warp per block, a lane per column); then
+// T21 = -T22 A21 T11 for the two 64-blocks at once and for the whole, on the
+// tensor cores with both operands as two bf16 terms (A21 and T22 in tensor
+// memory, T11 and A21 T11 as images).  A dozen dependent passes of little work
+// each, bound by their latency: three blocks share an SM (66 KB, 128
+// tensor-memory columns: K K^T, whose columns the operands [0, 64) and the
+// products [64, 128) take once A is in registers and shared memory).
+constexpr int kInvThreads = 256;
+constexpr int kLd = 36;                     // floats per row of a diagonal block
+constexpr uint32_t kBi = 8192;              // lo term of the products' images (64 rows)
+constexpr uint32_t kIDiag = kBlk;           // float[4][32][kLd]
+constexpr uint32_t kIGc = 4 * kBlk;
+constexpr uint32_t kIBeta = kIGc + 1024;
+constexpr uint32_t kICol = kIBeta + 512;    // beta times the column's factor
+constexpr uint32_t kIBar = kICol + 512;
+constexpr uint32_t kISmem = kIBar + 64;
 
-__global__ void __launch_bounds__(kThreads, 2)
-gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   GdnProblem p, const float* __restrict__ g, const float* __restrict__ beta,
-                   GdnTcWs w, int transposed) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+// kT: also Tinv^T.
+template <bool kT>
+__global__ void __launch_bounds__(kInvThreads, 3)
+gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
+                      const float* __restrict__ g, const float* __restrict__ beta, GdnTcWs w) {
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  float2* gc = reinterpret_cast<float2*>(smem + kOffGc);
-  float* sbeta = reinterpret_cast<float*>(smem + kOffBeta);
-  float* slam = reinterpret_cast<float*>(smem + kOffLam);
-  uint8_t* img = smem + kOffR;
-  const uint32_t ka = sbase + kOffK, ra = sbase + kOffR;
-  const uint32_t bar_k = sbase + kOffBar, bar = bar_k + 8, bar_v = bar_k + 16;
-  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
+  float2* gc = reinterpret_cast<float2*>(smem + kIGc);
+  float* sbeta = reinterpret_cast<float*>(smem + kIBeta);
+  float* scol = reinterpret_cast<float*>(smem + kICol);
+  const uint32_t bar_k = sbase + kIBar, bar = bar_k + 8;
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kIBar + 32);
   const int c = blockIdx.x, bh = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
   const int t0 = c * kGdnL, n = min(kGdnL, p.T - t0);
@@ -58,14 +52,13 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   if (tid == 0) {
     mbar_init(bar_k, 1);
     mbar_init(bar, 1);
-    mbar_init(bar_v, 1);
     fence_barrier_init();
     mbar_expect_tx(bar_k, slabs * kBlk);
     for (int s = 0; s < slabs; ++s)
-      tma_load_3d(ka + s * kBlk, &tm_k, s * 64, t0, gdn_key_head(p, bh), bar_k);
+      tma_load_3d(sbase + s * kBlk, &tm_k, s * 64, t0, gdn_key_head(p, bh), bar_k);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32((const void*)slot), 256);
+    tmem_alloc(smem_u32((const void*)slot), 128);
     tmem_relinquish();
   }
   if (warp == 2) gdn_chunk_sums(g + (long)bh * p.T + t0, n, lane, gc, w.gc + cb * kGdnL);
@@ -80,58 +73,62 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
   bool ok = true;
   uint32_t phase = 0;
+  if (warp >= 4) scol[r] = sbeta[r] * gdn_col_factor(gc[r], 31);
 
   run_mma(bar, phase, ok, wt, 0x42, [&] {
     ok = mbar_wait(bar_k, 0, wt, 0x41);
     tc_fence_after();
-    constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
-    if (ok) mma_ss<false, false>(tmem, ka, ka, id, slabs, true);
+    if (ok) mma_ss<false, false>(tmem, sbase, sbase, idesc_bf16(128, 128, 0, 0), slabs, true);
   });
   const float2 gr = gc[r];
-  const float dec = sbeta[r] * gdn_decay(gc[kGdnL - 1], gr);
-  if (h == 0) slam[r] = gdn_exp(gr);
-  // 32 elements of A's row r from column s0
-  auto a_row = [&](int s0, float (&x)[32]) {
+  // the terms of block b (columns 32 b ..) of A's row r, left of the diagonal's
+  auto a_block = [&](int b, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
     uint32_t v[32];
-    tmem_ld32(trow + s0, v);
+    tmem_ld32(trow + b * 32, v);
+    tmem_wait_ld();
+    const float f = gdn_decay(gr, gc[b * 32 + 31]);
+    float x[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = f * scol[b * 32 + e] * __uint_as_float(v[e]);
+    split_pack<32>(x, hi, lo);
+  };
+  float* diag = reinterpret_cast<float*>(smem + kIDiag);
+  float* dq = diag + q * 32 * kLd;  // [s][r] of block q
+  uint32_t hi1[16], lo1[16];        // A21 of the whole, columns 32 h ..
+  uint32_t hi0[16], lo0[16];        // A21 of the 64-blocks
+  if (q >= 2) a_block(h, hi1, lo1);
+  if (h == 0) {
+    uint32_t v[32];
+    tmem_ld32(trow + q * 32, v);
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-      const int s = s0 + e;
-      x[e] = s < r ? gdn_decay(gr, gc[s]) * sbeta[s] * __uint_as_float(v[e]) : 0.f;
+      const int s = q * 32 + e;
+      dq[e * kLd + lane] =
+          e < lane ? gdn_decay(gr, gc[s]) * sbeta[s] * __uint_as_float(v[e]) : 0.f;
     }
-  };
-  // A operand of the inversion: 64 inner columns, hi at 128, lo at 160
-  auto put_a32 = [&](int col, const float (&x)[32]) {
-    uint32_t hi[16], lo[16];
-    split_pack<32>(x, hi, lo);
-    tmem_st16(trow + 128 + col, hi);
-    tmem_st16(trow + 160 + col, lo);
-  };
-  float* diag = reinterpret_cast<float*>(smem + kOffDiag);
-  float* dq = diag + q * 32 * kLd;  // [s][r] of block q
+  } else if (q & 1) {
+    a_block(q - 1, hi0, lo0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   if (h == 0) {
-    // the diagonal block: column s of A at [s], then the inverse's column at [s]
-    {
-      float x[32];
-      a_row(q * 32, x);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) dq[e * kLd + lane] = x[e];
-    }
-    __syncwarp();
+    // column `lane` of the block's inverse: once x_s is known its multiples leave
+    // all later rows (independent products)
     float x[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = i == lane ? 1.f : 0.f;
 #pragma unroll
     for (int s = 0; s < 31; ++s) {
-      float a[32];
 #pragma unroll
       for (int r4 = (s + 1) / 4; r4 < 8; ++r4) {
         const float4 v = *reinterpret_cast<const float4*>(dq + s * kLd + r4 * 4);
-        a[4 * r4] = v.x; a[4 * r4 + 1] = v.y; a[4 * r4 + 2] = v.z; a[4 * r4 + 3] = v.w;
-      }
+        const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = s + 1; i < 32; ++i) x[i] = fmaf(-a[i], x[s], x[i]);
+        for (int i = 0; i < 4; ++i)
+          if (4 * r4 + i > s) x[4 * r4 + i] = fmaf(-a[i], x[s], x[4 * r4 + i]);
+      }
     }
     __syncwarp();  // every lane has read the block
 #pragma unroll
@@ -139,13 +136,14 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       *reinterpret_cast<float4*>(dq + lane * kLd + r4 * 4) =
           make_float4(x[4 * r4], x[4 * r4 + 1], x[4 * r4 + 2], x[4 * r4 + 3]);
   } else if (q & 1) {
-    // A21 of the 64-blocks: inner columns 0..31 the first block's, 32..63 the second's
-    float x[32];
-    a_row((q - 1) * 32, x);
-    put_a32(q == 3 ? 16 : 0, x);
+    // inner columns 0..31 are the first 64-block's, 32..63 the second's
+    const int at = q == 3 ? 16 : 0;
+    tmem_st16(trow + at, hi0);
+    tmem_st16(trow + 32 + at, lo0);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = 0.f;
-    put_a32(q == 3 ? 0 : 16, x);
+    for (int e = 0; e < 16; ++e) hi0[e] = 0u;
+    tmem_st16(trow + 16 - at, hi0);
+    tmem_st16(trow + 48 - at, hi0);
   }
   __syncthreads();
   // the image's rows: 0..31 and 32..63 are those of diagonal blocks 0 and 2
@@ -155,8 +153,8 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = d[(8 * cc + e) * kLd + (kr & 31)];
-    put8(img, kBi, kr, cc, x);
-    put8(img, kBi, kr, cc + 4, x);  // columns 32..63 of the product are not used
+    put8(smem, kBi, kr, cc, x);
+    put8(smem, kBi, kr, cc + 4, x);  // columns 32..63 of the product are not used
   }
   auto inv_mma = [&] {
     constexpr uint32_t id = idesc_bf16(128, 64, 0, 1);
@@ -164,222 +162,333 @@ gdn_tc_prep_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     for (int t = 0; t < 3; ++t)
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ts(tmem + 192, tmem + 128 + (t == 1 ? 32 : 0) + kk * 8,
-                    mnmaj(ra + (t == 2 ? kBi : 0u), kk), id, (t | kk) != 0);
+        mma_bf16_ts(tmem + 64, tmem + (t == 1 ? 32 : 0) + kk * 8,
+                    mnmaj(sbase + (t == 2 ? kBi : 0u), kk), id, (t | kk) != 0);
   };
   run_mma(bar, phase, ok, wt, 0x43, inv_mma);
   if (q & 1) {
     uint32_t v[16];
-    tmem_ld16(trow + 192 + h * 16, v);
+    tmem_ld16(trow + 64 + h * 16, v);
     tmem_wait_ld();
     const int kr = (q >> 1) * 32 + lane;
-    put8(img, kBi, kr, h * 2, reinterpret_cast<const float*>(v));
-    put8(img, kBi, kr, h * 2 + 1, reinterpret_cast<const float*>(v) + 8);
+    put8(smem, kBi, kr, h * 2, reinterpret_cast<const float*>(v));
+    put8(smem, kBi, kr, h * 2 + 1, reinterpret_cast<const float*>(v) + 8);
     float x[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] = dq[(h * 16 + e) * kLd + lane];
     uint32_t hi[8], lo[8];
     split_pack<16>(x, hi, lo);
-    tmem_st8(trow + 128 + (q >> 1) * 16 + h * 8, hi);
-    tmem_st8(trow + 160 + (q >> 1) * 16 + h * 8, lo);
+    tmem_st8(trow + (q >> 1) * 16 + h * 8, hi);
+    tmem_st8(trow + 32 + (q >> 1) * 16 + h * 8, lo);
   }
   run_mma(bar, phase, ok, wt, 0x44, inv_mma);
   // x: columns 32 h .. of this row inside its 64-block of the inverse
-  float x[32], b[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] = b[e] = 0.f;
+  float x[32];
   if (h == 0 && (q & 1)) {
     uint32_t v[32];
-    tmem_ld32(trow + 192, v);
+    tmem_ld32(trow + 64, v);
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 32; ++e) x[e] = -__uint_as_float(v[e]);
   } else if (h == (q & 1)) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) x[e] = dq[e * kLd + lane];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = 0.f;
   }
   if (q < 2) {
 #pragma unroll
-    for (int cc = 0; cc < 4; ++cc) put8(img, kBi, r, h * 4 + cc, x + 8 * cc);
+    for (int cc = 0; cc < 4; ++cc) put8(smem, kBi, r, h * 4 + cc, x + 8 * cc);
   } else {
-    float a[32];
-    a_row(h * 32, a);
-    put_a32(h * 16, a);
+    tmem_st16(trow + h * 16, hi1);
+    tmem_st16(trow + 32 + h * 16, lo1);
   }
   run_mma(bar, phase, ok, wt, 0x45, inv_mma);
+  split_pack<32>(x, hi1, lo1);
   if (q >= 2) {
     uint32_t v[32];
-    tmem_ld32(trow + 192 + h * 32, v);
+    tmem_ld32(trow + 64 + h * 32, v);
     tmem_wait_ld();
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc)
-      put8(img, kBi, r - 64, h * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
-    put_a32(h * 16, x);
+      put8(smem, kBi, r - 64, h * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
+    tmem_st16(trow + h * 16, hi1);
+    tmem_st16(trow + 32 + h * 16, lo1);
   }
   run_mma(bar, phase, ok, wt, 0x46, inv_mma);
+  // the row's terms, without the identity: block b holds columns 32 b ..
+  uint4* dst = w.tinv + cb * 32 * 128 + r;
+  auto put_row = [&](int b, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+    if (b == q)  // the diagonal's one sits in hi
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (e == lane >> 1) hi[e] &= lane & 1 ? 0x0000ffffu : 0xffff0000u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 uh = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      const uint4 ul = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+      if (b <= q) {
+        dst[(b * 4 + i) * 128] = uh;
+        dst[(16 + b * 4 + i) * 128] = ul;
+      }
+      if (kT) {
+        const uint32_t off = (b >> 1) * kBlk + sw128_offset(r, (b & 1) * 4 + i);
+        *reinterpret_cast<uint4*>(smem + off) = uh;
+        *reinterpret_cast<uint4*>(smem + 2 * kBlk + off) = ul;
+      }
+    }
+  };
+  put_row((q >> 1) * 2 + h, hi1, lo1);
   if (q >= 2) {
     uint32_t v[32];
-    tmem_ld32(trow + 192 + h * 32, v);
+    tmem_ld32(trow + 64 + h * 32, v);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 32; ++e) b[e] = -__uint_as_float(v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      b[e] = x[e];
-      x[e] = 0.f;
-    }
-  }
-  // Now b: columns 32 h .. of row r of Tinv, x: columns 64 + 32 h ..
-  {
-    uint4* dst = w.tinv + cb * 32 * 128 + r;
-    uint32_t hi[16], lo[16];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float y[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        y[e] = 2 * half + h == q && e == lane ? 0.f : (half ? x : b)[e];
-      split_pack<32>(y, hi, lo);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = half * 8 + h * 4 + i;
-        const uint4 uh = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-        const uint4 ul = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-        if (j < 4 * (q + 1)) {
-          dst[j * 128] = uh;
-          dst[(16 + j) * 128] = ul;
-        }
-        if (transposed) {
-          *reinterpret_cast<uint4*>(img + half * kBlk + sw128_offset(r, h * 4 + i)) = uh;
-          *reinterpret_cast<uint4*>(img + (2 + half) * kBlk + sw128_offset(r, h * 4 + i)) = ul;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) y[e] = (half ? x : b)[e] * slam[half * 64 + h * 32 + e];
-      split_pack<32>(y, hi, lo);
-      tmem_st16(trow + half * 32 + h * 16, hi);
-      tmem_st16(trow + 64 + half * 32 + h * 16, lo);
-    }
-  }
-  // W = (Tinv Lam) K
-  const uint32_t nk = idesc_bf16(128, slabs * 64, 0, 1), nkt = idesc_bf16(128, slabs * 64, 1, 1);
-  run_mma(bar, phase, ok, wt, 0x47, [&] { mma_terms2(tmem + 128, tmem, ka, nk); });
-  if (transposed) {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(w.tinvt + cb * 32 * 128);
-    for (int i = warp; i < 128; i += 8) {
-      const int term = i >> 6, sb = (i >> 2) & 15, rg = i & 3;  // 8 columns s, 32 rows r
-      if (rg < sb >> 2) continue;
-      uint32_t v[4];
-      ldmatrix4_trans(ra + (term * 2 + (sb >> 3)) * kBlk + sw128_offset(rg * 32 + lane, sb & 7), v);
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        dst[((term * 16 + rg * 4 + m) * 128 + sb * 8 + (lane >> 2)) * 4 + (lane & 3)] = v[m];
-    }
-    __syncthreads();
-  }
-  // the image of D beta (columns in tensor memory), or its third term
-  auto put_scaled = [&](int blocks, bool rest) {
-    for (int s = 0; s < blocks; ++s) {
-      uint32_t v[32];
-      tmem_ld32(trow + 128 + s * 64 + h * 32, v);
-      tmem_wait_ld();
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = dec * __uint_as_float(v[8 * cc + e]);
-        if (!rest) {
-          put8(img + s * kBlk, 2 * kBlk, r, h * 4 + cc, y);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = third(y[e]);
-          put8_one(img + s * kBlk, r, h * 4 + cc, y);
-        }
-      }
-    }
-  };
-  auto kt_mma = [&](uint32_t d, uint32_t id) {
-    mma_ss<true, true>(d, ka, ra, id, 2, true);
-    mma_ss<true, true>(d, ka, ra + 2 * kBlk, id, 2, false);
-  };
-  put_scaled(slabs, false);
-  run_mma(bar, phase, ok, wt, 0x48, [&] { kt_mma(tmem + 128, nkt); });
-  for (int s = 0; s < slabs; ++s) {
-    uint32_t v[32];
-    tmem_ld32(trow + 128 + s * 64 + h * 32, v);
-    tmem_wait_ld();
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc)
-      put8(img + s * kBlk, 2 * kBlk, r, h * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
-  }
-  fence_proxy_async_smem();
-  __syncthreads();
-  if (tid == 0) {
-    uint8_t* dst = w.M + cb * 4 * kBlk;
-    for (int t = 0; t < 2; ++t)
-      bulk_store(dst + t * 2 * kBlk, ra + t * 2 * kBlk, slabs * kBlk);
-    tma_store_commit();
-    tma_store_wait_read_all();
-  }
-  // two value tiles at a time
-  for (int v0 = 0; v0 < w.nvt; v0 += 2) {
-    const int tiles = min(2, w.nvt - v0);
-    if (tid == 0) {  // the image has been read (above, or by the last products)
-      mbar_expect_tx(bar_v, tiles * kBlk);
-      for (int s = 0; s < tiles; ++s)
-        tma_load_3d(ra + s * kBlk, &tm_v, (v0 + s) * 64, t0, bh, bar_v);
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {  // Tinv, which N replaces
-      uint32_t hi[16], lo[16];
-      split_pack<32>(half ? x : b, hi, lo);
-      tmem_st16(trow + half * 32 + h * 16, hi);
-      tmem_st16(trow + 64 + half * 32 + h * 16, lo);
-    }
-    const uint32_t nv = idesc_bf16(128, tiles * 64, 0, 1), nvt = idesc_bf16(128, tiles * 64, 1, 1);
-    run_mma(bar, phase, ok, wt, 0x49, [&] {
-      ok = mbar_wait(bar_v, (v0 >> 1) & 1, wt, 0x4a);
-      tc_fence_after();
-      if (ok) mma_terms2(tmem + 128, tmem, ra, nv);
-    });
-    put_scaled(tiles, false);
-    run_mma(bar, phase, ok, wt, 0x4b, [&] { kt_mma(tmem, nvt); });
-    put_scaled(tiles, true);
-    run_mma(bar, phase, ok, wt, 0x4c, [&] { mma_ss<true, true>(tmem, ka, ra, nvt, 2, false); });
-    for (int s = 0; s < tiles; ++s) {
-      uint32_t v[32];
-      tmem_ld32(trow + s * 64 + h * 32, v);
-      tmem_wait_ld();
-      float4* dst = w.N + ((cb * w.nvt + v0 + s) * 16 + h * 8) * 128 + r;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        dst[e * 128] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                   __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-    }
+    for (int e = 0; e < 32; ++e) v[e] ^= 0x80000000u;
+    split_pack<32>(reinterpret_cast<const float*>(v), hi1, lo1);
+    put_row(h, hi1, lo1);
   }
   tc_fence_before();
   __syncthreads();
+  if (kT) {  // 8 columns s by 32 rows r at a time; columns of rows above are zero
+    uint32_t* out = reinterpret_cast<uint32_t*>(w.tinvt + cb * 32 * 128);
+    for (int i = warp; i < 128; i += 8) {
+      const int term = i >> 6, sb = (i >> 2) & 15, rg = i & 3;
+      if (rg < sb >> 2) continue;
+      uint32_t v[4];
+      ldmatrix4_trans(
+          sbase + (term * 2 + (sb >> 3)) * kBlk + sw128_offset(rg * 32 + lane, sb & 7), v);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        out[((term * 16 + rg * 4 + m) * 128 + sb * 8 + (lane >> 2)) * 4 + (lane & 3)] = v[m];
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 128);
   }
-  if (tid == 0) tma_store_wait_all();
+}
+
+// ------------------------------------------------------------------ M and N
+// Per (bh, chunk, up to 128 value columns): two rounds,
+//   {W = (Tinv Lam) K, U = Tinv V}, {M = K^T (D beta W), N = K^T (D beta U)}.
+// 72 products of 128 x 128 x 16 (about 4900 cycles).  M only with the first pair
+// of value tiles.  Tensor memory: Tinv [0, 128), W then M [128, 256), U then N
+// [256, 384), Tinv Lam [384, 512).
+constexpr uint32_t kMV = 2 * kBlk, kMW = 4 * kBlk, kMU = 8 * kBlk;
+constexpr uint32_t kMLam = 14 * kBlk;
+constexpr uint32_t kMBar = kMLam + 512;
+constexpr uint32_t kMSmem = kMBar + 64;
+static_assert(kMSmem <= 227 * 1024, "shared memory");
+
+__global__ void __launch_bounds__(kGdnThreads, 1)
+gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 GdnProblem p, const float* __restrict__ beta, GdnTcWs w) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  float* slam = reinterpret_cast<float*>(smem + kMLam);
+  const uint32_t ka = sbase, va = sbase + kMV, wa = sbase + kMW, ua = sbase + kMU;
+  const uint32_t bar_k = sbase + kMBar, bar_v = bar_k + 8;
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kMBar + 32);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
+  const bool row = tid < kGdnRows, lead = tid == kGdnRows;
+  const int slabs = (p.DK + 63) / 64;
+  const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
+  GdnRounds rd{bar_k + 16, 0u, true, Problem{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls}};
+  auto load_k = [&](const GdnItem& x) {
+    mbar_expect_tx(bar_k, slabs * kBlk);
+    for (int s = 0; s < slabs; ++s)
+      tma_load_3d(ka + s * kBlk, &tm_k, s * 64, x.t0, gdn_key_head(p, x.bh), bar_k);
+  };
+  auto load_v = [&](const GdnItem& x) {
+    mbar_expect_tx(bar_v, x.tiles * kBlk);
+    for (int v = 0; v < x.tiles; ++v)
+      tma_load_3d(va + v * kBlk, &tm_v, (x.vt + v) * 64, x.t0, x.bh, bar_v);
+  };
+  uint4 ti[8];
+  float2 ngc, ngl;
+  float nbt;
+  auto load_rows = [&](const GdnItem& x) {
+    load_tinv(w.tinv + x.cb * 32 * 128, r, h, h <= q, ti);
+    ngc = w.gc[x.cb * kGdnL + r];
+    ngl = w.gc[x.cb * kGdnL + kGdnL - 1];
+    nbt = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
+  };
+
+  GdnItem x(blockIdx.x, p, w);
+  if (lead) {
+    for (int i = 0; i < 3; ++i) mbar_init(bar_k + 8 * i, 1);
+    fence_barrier_init();
+    load_k(x);
+    load_v(x);
+  }
+  if (!row) {
+    __syncwarp();
+    tmem_alloc(smem_u32((const void*)slot), 512);
+    tmem_relinquish();
+  } else {
+    load_rows(x);
+    if (h == 0) slam[r] = gdn_exp(ngc);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16), trow = tlane + h * 32;
+  uint32_t in_phase = 0;
+
+  for (long i = blockIdx.x; i < items; i += gridDim.x, in_phase ^= 1) {
+    const bool more = i + gridDim.x < items;
+    const GdnItem nx(more ? i + gridDim.x : i, p, w);
+    const bool first = x.vt == 0;
+    const uint32_t nk = idesc_bf16(128, slabs * 64, 0, 1), nkt = idesc_bf16(128, slabs * 64, 1, 1);
+    const uint32_t nv = idesc_bf16(128, x.tiles * 64, 0, 1),
+                   nvt = idesc_bf16(128, x.tiles * 64, 1, 1);
+    float dec = 0.f;
+    if (row) {
+      dec = nbt * gdn_decay(ngl, ngc);
+      add_identity(r, h, ti);
+      put_tinv(tlane, h, ti);
+      if (first) {  // Tinv Lam
+        uint32_t hi[16], lo[16];
+        if (h <= q) {
+          float y[32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float a[8], b[8];
+            unpack8(ti[k], a);
+            unpack8(ti[4 + k], b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[8 * k + e] = (a[e] + b[e]) * slam[h * 32 + 8 * k + e];
+          }
+          split_pack<32>(y, hi, lo);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
+        }
+        tmem_st16(tlane + 384 + h * 16, hi);
+        tmem_st16(tlane + 448 + h * 16, lo);
+      }
+      if (more) load_rows(nx);
+    }
+    if (lead) tma_store_wait_read_all();  // M of the item before has left
+    gdn_round(
+        rd, 0x47,
+        [&] {
+          rd.ok = mbar_wait(bar_k, in_phase, rd.wt, 0x48);
+          rd.ok = rd.ok && mbar_wait(bar_v, in_phase, rd.wt, 0x49);
+          tc_fence_after();
+          if (!rd.ok) return;
+          if (first) mma_terms2(tmem + 128, tmem + 384, ka, nk);
+          mma_terms2(tmem + 256, tmem, va, nv);
+        },
+        gdn_nothing, gdn_nothing,
+        [&] {
+          if (more) load_v(nx);
+        });
+    uint32_t v[32];
+    if (row) {
+      if (first && h < 2 * slabs) {
+        tmem_ld32(trow + 128, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = dec * __uint_as_float(v[8 * cc + e]);
+          put8(smem + kMW + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+        }
+      }
+      if (h < 2 * x.tiles) {
+        tmem_ld32(trow + 256, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = dec * __uint_as_float(v[8 * cc + e]);
+          put8x3(smem + kMU + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+        }
+      }
+    }
+    gdn_round(
+        rd, 0x4a,
+        [&] {
+          if (first)
+            for (int t = 0; t < 2; ++t)
+              mma_ss<true, true>(tmem + 128, ka, wa + 2 * t * kBlk, nkt, 2, t == 0);
+          for (int t = 0; t < 3; ++t)
+            mma_ss<true, true>(tmem + 256, ka, ua + 2 * t * kBlk, nvt, 2, t == 0);
+        },
+        gdn_nothing, gdn_nothing,
+        [&] {
+          if (more) load_k(nx);
+        });
+    if (row) {
+      if (first && h < 2 * slabs) {
+        tmem_ld32(trow + 128, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc)
+          put8(smem + kMW + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc,
+               reinterpret_cast<const float*>(v) + 8 * cc);
+      }
+      if (h < 2 * x.tiles) {
+        tmem_ld32(trow + 256, v);
+        tmem_wait_ld();
+        float4* dst = w.N + ((x.cb * w.nvt + x.vt + (h >> 1)) * 16 + (h & 1) * 8) * 128 + r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[e * 128] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                     __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+      }
+      if (more && h == 0) slam[r] = gdn_exp(ngc);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (lead && first) {
+      for (int t = 0; t < 2; ++t)
+        bulk_store(w.M + (x.cb * 4 + 2 * t) * kBlk, wa + 2 * t * kBlk, slabs * kBlk);
+      tma_store_commit();
+    }
+    x = nx;
+  }
+  if (lead) tma_store_wait_all();
+  __syncthreads();
+  if (!row) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_gdn_tc_prep(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
-                               bool transposed, cudaStream_t st) {
+cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
+                                  cudaStream_t st) {
+  CUtensorMap tk;
+  if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL))
+    return cudaErrorInvalidValue;
+  auto kern = w.tinvt ? gdn_tc_inverse_kernel<true> : gdn_tc_inverse_kernel<false>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kISmem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(w.NC, p.BH), kInvThreads, kISmem, st>>>(tk, p, x.g, x.beta, w);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gdn_tc_mn(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
+                             cudaStream_t st) {
   CUtensorMap tk, tv;
   if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL) ||
       !encode_tmap_bf16_3d(&tv, x.V, p.DV, p.T, p.BH, 64, kGdnL))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(
-      gdn_tc_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      gdn_tc_mn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMSmem);
   if (e != cudaSuccess) return e;
-  gdn_tc_prep_kernel<<<dim3(w.NC, p.BH), kThreads, kSmem, st>>>(tk, tv, p, x.g, x.beta, w,
-                                                                transposed);
+  gdn_tc_mn_kernel<<<gdn_blocks(p, w), kGdnThreads, kMSmem, st>>>(tk, tv, p, x.beta, w);
   return cudaGetLastError();
 }
 
