@@ -25,8 +25,9 @@ constexpr uint32_t kOffQ = 0, kOffK = 2 * kBlk, kOffS = 4 * kBlk, kOffZ = 8 * kB
 constexpr uint32_t kOffV = 12 * kBlk;
 constexpr uint32_t kOffGc = 14 * kBlk;            // float2[128]
 constexpr uint32_t kOffBeta = kOffGc + 1024;      // float[128]
-constexpr uint32_t kOffCol = kOffBeta + 512;      // float[128], beta times the column's factor
-constexpr uint32_t kOffBar = kOffCol + 512;
+constexpr uint32_t kOffCol = kOffBeta + 512;      // float[2][128], beta times the column's factor
+                                                  // (below the diagonal's block, in it)
+constexpr uint32_t kOffBar = kOffCol + 1024;
 constexpr uint32_t kSmem = kOffBar + 64;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -70,8 +71,7 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint4 ti[8];
   float2 ng;
   float nb;
-  auto load_rows = [&](const GdnItem& x) {
-    load_tinv(w.tinv + x.cb * 32 * 128, r, h, h <= q, ti);
+  auto load_gates = [&](const GdnItem& x) {
     ng = w.gc[x.cb * kGdnL + r];
     nb = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
   };
@@ -88,7 +88,7 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
   } else {
-    load_rows(x);
+    load_gates(x);
   }
   tc_fence_before();
   __syncthreads();
@@ -110,10 +110,9 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         gc[r] = gr;
         sbeta[r] = nb;
         scol[r] = nb * gdn_col_factor(gr, 31);
+        scol[128 + r] = __fdividef(nb, gdn_col_factor(gr, 0));
       }
-      add_identity(r, h, ti);
-      put_tinv(tlane, h, ti);
-      if (more) load_rows(nx);
+      load_tinv(w.tinv + x.cb * 32 * 128, r, h, h <= q, ti);  // for the second round
     }
     if (lead) tma_store_wait_read_all();  // what the image held has left
     gdn_round(
@@ -139,6 +138,11 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         });
     const float lam = gdn_exp(gr);
     uint32_t v[32];
+    if (row) {
+      add_identity(r, h, ti);
+      put_tinv(tlane, h, ti);
+      if (more) load_gates(nx);
+    }
     if (cols) {
       tmem_ld32(trow + 256, v);
       tmem_wait_ld();
@@ -165,16 +169,18 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             float s[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(v[e]);
-            if (h == q) {
+            if (h == q && gc[h * 32].x - gc[h * 32 + 31].x > kGdnFlat) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const int k = h * 32 + e;
                 s[e] = e <= lane ? gdn_decay(gr, gc[k]) * sbeta[k] * s[e] : 0.f;
               }
             } else {
-              const float f = gdn_decay(gr, gc[h * 32 + 31]);
+              const bool d = h == q;
+              const float f = gdn_decay(gr, gc[h * 32 + (d ? 0 : 31)]);
+              const float* sc = scol + (d ? 128 : 0) + h * 32;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[e] *= f * scol[h * 32 + e];
+              for (int e = 0; e < 32; ++e) s[e] = d && e > lane ? 0.f : s[e] * (f * sc[e]);
             }
             split_pack<32>(s, hi, lo);
           } else {

@@ -124,17 +124,14 @@ __device__ __forceinline__ uint64_t mnmaj(uint32_t img, int kk) {
   return sdesc_sw128(img + kk * 2048, kBlk, 1024);
 }
 
-// The two bf16 terms of eight fp32 values.
-__device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    h[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-    l[e] = pack_bf16x2(x[2 * e] - __uint_as_float(h[e] << 16),
-                       x[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+// Two values to a bf16 pair, and what the rounding left of them.  (Conversions
+// of pairs: of single values they run at a quarter of the rate, which made a pass
+// that forms three terms of 128 x 128 values take 2700 cycles in place of 1400.)
+__device__ __forceinline__ uint32_t take_pair(float& a, float& b) {
+  const uint32_t h = pack_bf16x2(a, b);
+  a -= __uint_as_float(h << 16);
+  b -= __uint_as_float(h & 0xffff0000u);
+  return h;
 }
 // The terms of N values, packed in pairs.
 template <int N>
@@ -142,38 +139,33 @@ __device__ __forceinline__ void split_pack(const float* x, uint32_t (&hi)[N / 2]
                                            uint32_t (&lo)[N / 2]) {
 #pragma unroll
   for (int e = 0; e < N / 2; ++e) {
-    hi[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-    lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(hi[e] << 16),
-                        x[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+    float a = x[2 * e], b = x[2 * e + 1];
+    hi[e] = take_pair(a, b);
+    lo[e] = pack_bf16x2(a, b);
   }
 }
-
-// Eight values as 16-byte piece c of row r of a block; the lo term lies `term`
-// bytes behind the hi term.
-__device__ __forceinline__ void put8(uint8_t* img, uint32_t term, int r, int c, const float* x) {
-  uint4 hi, lo;
-  split8(x, hi, lo);
-  *reinterpret_cast<uint4*>(img + sw128_offset(r, c)) = hi;
-  *reinterpret_cast<uint4*>(img + term + sw128_offset(r, c)) = lo;
-}
-// The third bf16 term of a value.
-__device__ __forceinline__ float third(float x) {
-  x -= __bfloat162float(__float2bfloat16_rn(x));
-  return x - __bfloat162float(__float2bfloat16_rn(x));
-}
-// Eight values, rounded, as a piece of a block.
-__device__ __forceinline__ void put8_one(uint8_t* img, int r, int c, const float* x) {
-  *reinterpret_cast<uint4*>(img + sw128_offset(r, c)) =
-      make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                 pack_bf16x2(x[6], x[7]));
-}
-// Eight values as a piece of three terms, `term` bytes apart.
-__device__ __forceinline__ void put8x3(uint8_t* img, uint32_t term, int r, int c, const float* x) {
-  put8(img, term, r, c, x);
+// Eight values as 16-byte piece c of row r of a block in kTerms terms, `term`
+// bytes apart; kFrom: the first term that is written.
+template <int kTerms, int kFrom = 0>
+__device__ __forceinline__ void put_terms(uint8_t* img, uint32_t term, int r, int c,
+                                          const float* x) {
   float y[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = third(x[e]);
-  put8_one(img + 2 * term, r, c, y);
+  for (int e = 0; e < 8; ++e) y[e] = x[e];
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    uint32_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = t + 1 < kTerms ? take_pair(y[2 * e], y[2 * e + 1])
+                            : pack_bf16x2(y[2 * e], y[2 * e + 1]);
+    if (t >= kFrom)
+      *reinterpret_cast<uint4*>(img + (t - kFrom) * term + sw128_offset(r, c)) =
+          make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+__device__ __forceinline__ void put8(uint8_t* img, uint32_t term, int r, int c, const float* x) {
+  put_terms<2>(img, term, r, c, x);
 }
 // Eight bf16 values of a row.
 __device__ __forceinline__ void unpack8(uint4 u, float* x) {
@@ -214,6 +206,9 @@ __device__ __forceinline__ bool elect_one() {
 // below one, e^{gc_r - gc_m} e^{gc_m - gc_s} with m the block's last token (or,
 // transposed, e^{gc_t - gc_m} e^{gc_m - gc_r} with m its first), so that one
 // exponential per row and one per column replace one per element.
+// In the diagonal's block the two would be above and below one: exact as long as
+// the block's whole decay stays within fp32 (kGdnFlat), else one by one.
+constexpr float kGdnFlat = 60.f;
 // Factor of column s, by the thread of token s (a warp holds a block).
 __device__ __forceinline__ float gdn_col_factor(float2 g, int m) {
   const float2 gm = make_float2(__shfl_sync(0xffffffffu, g.x, m), __shfl_sync(0xffffffffu, g.y, m));

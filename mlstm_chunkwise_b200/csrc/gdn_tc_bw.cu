@@ -22,8 +22,8 @@ using namespace tc;
 // terms: two go under the first round, the third under the third.
 constexpr uint32_t kZDh = 4 * kBlk, kZL = 6 * kBlk, kZW = 10 * kBlk;
 constexpr uint32_t kZGc = 14 * kBlk;
-constexpr uint32_t kZCol = kZGc + 1024;  // float[128]: the columns' factors
-constexpr uint32_t kZBar = kZCol + 512;
+constexpr uint32_t kZCol = kZGc + 1024;  // float[2][128]: the columns' factors
+constexpr uint32_t kZBar = kZCol + 1024;
 constexpr uint32_t kZSmem = kZBar + 64;
 static_assert(kZSmem <= 227 * 1024, "shared memory");
 
@@ -69,7 +69,6 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   float2 ngc;
   float nbt;
   auto load_rows = [&](const GdnItem& x) {
-    load_tinv(w.tinvt + x.cb * 32 * 128, r, h, h >= q, ti);
     ngc = w.gc[x.cb * kGdnL + r];
     nbt = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
   };
@@ -108,10 +107,10 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       bt = nbt;
       if (h == 0) {
         gc[r] = gr;
-        scol[r] = gdn_col_factor(gr, 0);
+        const float f = gdn_col_factor(gr, 0);
+        scol[r] = f;
+        scol[128 + r] = __fdividef(1.f, gdn_col_factor(gr, 31));
       }
-      add_identity(r, h, ti);
-      put_tinv(tlane + 128, h, ti);
       if (more) load_rows(nx);
     }
     const float lam = gdn_exp(gr), sl = p.scale * lam;
@@ -145,14 +144,16 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         float g[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) g[e] = __uint_as_float(v[e]);
-        if (h == q) {
+        if (h == q && gc[h * 32].x - gc[h * 32 + 31].x > kGdnFlat) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             g[e] = e >= lane ? gdn_decay(gc[h * 32 + e], gr) * g[e] : 0.f;
         } else {
-          const float f = gdn_decay(gc[h * 32], gr);
+          const bool d = h == q;
+          const float f = gdn_decay(gc[h * 32 + (d ? 31 : 0)], gr);
+          const float* sc = scol + (d ? 128 : 0) + h * 32;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) g[e] *= f * scol[h * 32 + e];
+          for (int e = 0; e < 32; ++e) g[e] = d && e < lane ? 0.f : g[e] * (f * sc[e]);
         }
         split_pack<32>(g, hi, lo);
       } else {
@@ -161,6 +162,7 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
       tmem_st16(trow, hi);
       tmem_st16(trow + 16, lo);
+      load_tinv(w.tinvt + x.cb * 32 * 128, r, h, h >= q, ti);  // for the third round
     }
     gdn_round(
         rd, 0x72,
@@ -185,6 +187,10 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         put8(smem + kZW + at, 2 * kBlk, r, (h & 1) * 4 + cc, y);
       }
     };
+    if (row) {
+      add_identity(r, h, ti);
+      put_tinv(tlane + 128, h, ti);
+    }
     if (cols) {
       tmem_ld32(trow + 256, v);
       tmem_wait_ld();
@@ -201,8 +207,8 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                                     sw128_offset(r, (h & 1) * 4 + cc)),
                     y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = third(y[e] * sl);
-            put8_one(smem + kZL + at, r, (h & 1) * 4 + cc, y);
+            for (int e = 0; e < 8; ++e) y[e] *= sl;
+            put_terms<3, 2>(smem + kZL + at, 0, r, (h & 1) * 4 + cc, y);
           }
         },
         gdn_nothing, gdn_nothing);
@@ -283,7 +289,6 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
   float2 ngc, ngl;
   float nbt;
   auto load_rows = [&](const GdnItem& x) {
-    load_tinv(w.tinvt + x.cb * 32 * 128, r, h, h >= q, ti);
     ngc = w.gc[x.cb * kGdnL + r];
     ngl = w.gc[x.cb * kGdnL + kGdnL - 1];
     nbt = r < x.n ? beta[(long)x.bh * p.T + x.t0 + r] : 0.f;
@@ -324,8 +329,7 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (row) {
       dec = gdn_decay(ngl, ngc);
       bd = nbt * dec;
-      add_identity(r, h, ti);
-      put_tinv(tlane, h, ti);
+      load_tinv(w.tinvt + x.cb * 32 * 128, r, h, h >= q, ti);  // for the second round
       if (more) load_rows(nx);
     }
     float4 z0[8];
@@ -346,6 +350,10 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
           if (more) load_tiles(nx);
         });
     uint32_t v[32];
+    if (row) {
+      add_identity(r, h, ti);
+      put_tinv(tlane, h, ti);
+    }
     if (cols) {
       tmem_ld32(trow + 128, v);
       tmem_wait_ld();
@@ -430,7 +438,7 @@ constexpr uint32_t kGDot = kGDiag + 512;          // float[16]
 constexpr uint32_t kGGc = 14 * kBlk;
 constexpr uint32_t kGBeta = kGGc + 1024;
 constexpr uint32_t kGCol = kGBeta + 512;
-constexpr uint32_t kGBar = kGCol + 512;
+constexpr uint32_t kGBar = kGCol + 1024;
 constexpr uint32_t kGSmem = kGBar + 64;
 static_assert(kGSmem <= 227 * 1024, "shared memory");
 
@@ -555,6 +563,7 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
         gc[r] = gr;
         sbeta[r] = nbt;
         scol[r] = gdn_col_factor(gr, 31);
+        scol[128 + r] = __fdividef(1.f, gdn_col_factor(gr, 0));
       }
       if (more) load_rows(next);
     }
@@ -608,18 +617,21 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
     float rh[32], eh[32];
     if (lower) {
       uint32_t a[16];
-      const float f = gdn_decay(gr, gc[h * 32 + 31]);
+      const bool d = h == q, steep = d && gc[h * 32].x - gc[h * 32 + 31].x > kGdnFlat;
+      const float f = gdn_decay(gr, gc[h * 32 + (d ? 0 : 31)]);
+      const float* sc = scol + (d ? 128 : 0) + h * 32;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float g[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int k = half * 16 + e;
-          if (h == q)
-            g[e] = k <= lane ? gdn_decay(gr, gc[h * 32 + k]) : 0.f;
-          else
-            g[e] = f * scol[h * 32 + k];
+          g[e] = d && k > lane ? 0.f : f * sc[k];
         }
+        if (steep)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            g[e] = half * 16 + e <= lane ? gdn_decay(gr, gc[h * 32 + half * 16 + e]) : 0.f;
         tmem_ld16(trow + half * 16, a);
         tmem_wait_ld();
 #pragma unroll

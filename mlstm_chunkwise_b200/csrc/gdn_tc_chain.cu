@@ -128,13 +128,7 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
       uint8_t* img = smem + kOffS + (i & 1) * kTerms * kBlk;
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        put8(img, kBlk, r, h * 2 + cc, s + 8 * cc);
-        if (kRev) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = third(s[8 * cc + e]);
-          put8_one(img + 2 * kBlk, r, h * 2 + cc, x);
-        }
+        put_terms<kTerms>(img, kBlk, r, h * 2 + cc, s + 8 * cc);
       }
       fence_proxy_async_smem();
       tc_fence_before();

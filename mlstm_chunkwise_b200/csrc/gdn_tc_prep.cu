@@ -371,7 +371,6 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         tmem_st16(tlane + 384 + h * 16, hi);
         tmem_st16(tlane + 448 + h * 16, lo);
       }
-      if (more) load_rows(nx);
     }
     if (lead) tma_store_wait_read_all();  // M of the item before has left
     gdn_round(
@@ -409,7 +408,7 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = dec * __uint_as_float(v[8 * cc + e]);
-          put8x3(smem + kMU + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+          put_terms<3>(smem + kMU + (h >> 1) * kBlk, 2 * kBlk, r, (h & 1) * 4 + cc, y);
         }
       }
     }
@@ -422,7 +421,10 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           for (int t = 0; t < 3; ++t)
             mma_ss<true, true>(tmem + 256, ka, ua + 2 * t * kBlk, nvt, 2, t == 0);
         },
-        gdn_nothing, gdn_nothing,
+        [&] {
+          if (more) load_rows(nx);
+        },
+        gdn_nothing,
         [&] {
           if (more) load_k(nx);
         });
