@@ -51,13 +51,14 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   const int slabs = (p.DK + 63) / 64;
   const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
   GdnRounds rd{bar_in + 16, 0u, true, Problem{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls}};
-  auto load_tiles = [&](const GdnItem& x) {
+  auto load_tiles = [&](const GdnItem& x, bool wait) {
     mbar_expect_tx(bar_in, slabs * ((kH ? 2 : 1) * kBlk + x.tiles * 2 * 8192));
     const int kh = gdn_key_head(p, x.bh);
     for (int s = 0; s < slabs; ++s) {
       tma_load_3d(ka + s * kBlk, &tm_k, s * 64, x.t0, kh, bar_in);
       if (kH) tma_load_3d(qa + s * kBlk, &tm_q, s * 64, x.t0, kh, bar_in);
     }
+    if (wait) gdn_wait_stage();
     for (int v = 0; v < x.tiles; ++v)
       for (int t = 0; t < 2; ++t)
         bulk_load(sa + (2 * t + v) * kBlk, w.S + ((x.cb * w.nvt + x.vt + v) * 2 + t) * kBlk,
@@ -77,19 +78,20 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   };
 
   GdnItem x(blockIdx.x, p, w);
+  gdn_next_stage();
   if (lead) {
     for (int i = 0; i < 3; ++i) mbar_init(bar_in + 8 * i, 1);
     fence_barrier_init();
-    load_tiles(x);
     load_v(x);
+    load_tiles(x, true);
   }
   if (!row) {
     __syncwarp();
     tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
-  } else {
-    load_gates(x);
   }
+  gdn_wait_stage();
+  if (row) load_gates(x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -134,7 +136,7 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         },
         gdn_nothing,
         [&] {
-          if (more) load_tiles(nx);
+          if (more) load_tiles(nx, false);
         });
     const float lam = gdn_exp(gr);
     uint32_t v[32];
@@ -311,27 +313,65 @@ size_t carve(const GdnProblem& p, int parts, const void* base, GdnTcWs* w) {
 constexpr int kFwParts = kState | kInverse | kN;
 constexpr int kBwParts = kState | kKeep | kInverse | kN | kGrad;
 
-cudaError_t forward(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T, const GdnTcWs& w,
-                    cudaStream_t st) {
-  cudaError_t e = launch_gdn_tc_inverse(p, x, w, st);
-  if (e != cudaSuccess) return e;
-  if ((e = launch_gdn_tc_mn(p, x, w, st)) != cudaSuccess) return e;
-  if ((e = launch_gdn_tc_chain(p, false, x.C0, C_T, w, st)) != cudaSuccess) return e;
-  return launch_gdn_tc_out(p, x, H, w, st);
+bool map16(CUtensorMap* m, const void* base, int cols, int T, long heads) {
+  return encode_tmap_bf16_3d(m, base, cols, T, heads, 64, kGdnL);
 }
-cudaError_t backward(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, const GdnTcWs& w,
-                     cudaStream_t st) {
-  cudaError_t e = launch_gdn_tc_dz0(p, x, d, w, st);
+
+cudaError_t forward(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T, GdnMaps& m,
+                    const GdnTcWs& w, cudaStream_t st) {
+  const long kheads = (long)p.B * p.NHK;
+  if (!map16(&m.k, x.K, p.DK, p.T, kheads) || !map16(&m.q, x.Q, p.DK, p.T, kheads) ||
+      !map16(&m.v, x.V, p.DV, p.T, p.BH) || (H && !map16(&m.h, H, p.DV, p.T, p.BH)))
+    return cudaErrorInvalidValue;
+  if (!H) m.h = m.v;
+  cudaError_t e = launch_gdn_tc_inverse(p, x, m, w, st);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_gdn_tc_mn(p, x, m, w, st)) != cudaSuccess) return e;
+  if ((e = launch_gdn_tc_chain(p, false, x.C0, C_T, w, st)) != cudaSuccess) return e;
+  return launch_gdn_tc_out(p, x, m, H != nullptr, w, st);
+}
+// behind: forward() ran before, with m's Q and K.
+cudaError_t backward(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, bool behind,
+                     GdnMaps& m, const GdnTcWs& w, cudaStream_t st) {
+  const long kheads = (long)p.B * p.NHK;
+  if (!behind && (!map16(&m.k, x.K, p.DK, p.T, kheads) || !map16(&m.q, x.Q, p.DK, p.T, kheads)))
+    return cudaErrorInvalidValue;
+  if (!map16(&m.dh, d.dH, p.DV, p.T, p.BH) || !map16(&m.dv, d.dV, p.DV, p.T, p.BH))
+    return cudaErrorInvalidValue;
+  if (w.dq ? !encode_tmap_3d(&m.dq, w.dq, 4, p.DK, p.T, p.BH, 32, kGdnL, 128) ||
+                 !encode_tmap_3d(&m.dk, w.dk, 4, p.DK, p.T, p.BH, 32, kGdnL, 128)
+           : !map16(&m.dq, d.dQ, p.DK, p.T, kheads) || !map16(&m.dk, d.dK, p.DK, p.T, kheads))
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch_gdn_tc_dz0(p, x, m, behind, w, st);
   if (e != cudaSuccess) return e;
   if ((e = launch_gdn_tc_chain(p, true, d.dC_T, d.dC0, w, st)) != cudaSuccess) return e;
-  if ((e = launch_gdn_tc_dz(p, x, d, w, st)) != cudaSuccess) return e;
-  return launch_gdn_tc_grads(p, x, d, w, st);
+  if ((e = launch_gdn_tc_dz(p, x, m, w, st)) != cudaSuccess) return e;
+  return launch_gdn_tc_grads(p, x, d, m, w, st);
 }
 
 }  // namespace
 
 bool gdn_tc_supported(const GdnProblem& p) {
   return p.DK <= 128 && p.DK % 8 == 0 && p.DV % 8 == 0;
+}
+
+cudaError_t gdn_allow_smem(const void* kern, size_t smem) {
+  struct Seen {
+    const void* kern;
+    unsigned long long ctx;
+  };
+  static thread_local Seen seen[16] = {};  // more than there are kernels
+  unsigned long long id = 0;
+  const bool known = current_context_id(&id);
+  Seen* free_slot = nullptr;
+  for (Seen& s : seen) {
+    if (known && s.kern == kern && s.ctx == id) return cudaSuccess;
+    if (!free_slot && (!s.kern || s.kern == kern)) free_slot = &s;
+  }
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && known && free_slot) *free_slot = Seen{kern, id};
+  return e;
 }
 
 size_t gdn_tc_workspace(const GdnProblem& p, bool backward) {
@@ -351,51 +391,46 @@ int gdn_tc_launches(const GdnProblem& p, bool backward) {
   return backward ? 4 + gdn_tc_train_launches(p, true) : 4;
 }
 
-cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
-                              cudaStream_t st) {
-  CUtensorMap tq, tk, tv, th;
-  const uint64_t kheads = (uint64_t)p.B * p.NHK;
-  if (!encode_tmap_bf16_3d(&tq, x.Q, p.DK, p.T, kheads, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, kheads, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&tv, x.V, p.DV, p.T, p.BH, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&th, H ? H : x.V, p.DV, p.T, p.BH, 64, kGdnL))
-    return cudaErrorInvalidValue;
-  auto kern = !H ? gdn_tc_out_kernel<false, true>
-                 : w.y ? gdn_tc_out_kernel<true, true> : gdn_tc_out_kernel<true, false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<gdn_blocks(p, w), kGdnThreads, kSmem, st>>>(
-      tq, tk, tv, th, p, x.beta, w);
-  return cudaGetLastError();
+cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
+                              bool with_h, const GdnTcWs& w, cudaStream_t st) {
+  auto go = [&](auto* kern) {
+    return gdn_launch(kern, gdn_blocks(p, w), kGdnThreads, kSmem, true, st, m.q, m.k, m.v, m.h, p,
+                      x.beta, w);
+  };
+  if (!with_h) return go(&gdn_tc_out_kernel<false, true>);
+  return w.y ? go(&gdn_tc_out_kernel<true, true>) : go(&gdn_tc_out_kernel<true, false>);
 }
 
 cudaError_t launch_gdn_tc_fw(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T,
                              void* ws, cudaStream_t st) {
   GdnTcWs w{};
   carve(p, kFwParts, ws, &w);
-  return forward(p, x, H, C_T, w, st);
+  GdnMaps m;
+  return forward(p, x, H, C_T, m, w, st);
 }
 cudaError_t launch_gdn_tc_bw(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, void* ws,
                              cudaStream_t st) {
   GdnTcWs w{};
   carve(p, kBwParts, ws, &w);
-  const cudaError_t e = forward(p, x, nullptr, nullptr, w, st);
-  return e == cudaSuccess ? backward(p, x, d, w, st) : e;
+  GdnMaps m;
+  const cudaError_t e = forward(p, x, nullptr, nullptr, m, w, st);
+  return e == cudaSuccess ? backward(p, x, d, true, m, w, st) : e;
 }
 cudaError_t launch_gdn_tc_fw_train(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T,
                                    void* saved, void* ws, cudaStream_t st) {
   GdnTcWs w{};
   carve(p, kState | kKeep, saved, &w);
   carve(p, kInverse | kN, ws, &w);
-  return forward(p, x, H, C_T, w, st);
+  GdnMaps m;
+  return forward(p, x, H, C_T, m, w, st);
 }
 cudaError_t launch_gdn_tc_bw_saved(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
                                    const void* saved, void* ws, cudaStream_t st) {
   GdnTcWs w{};
   carve(p, kState | kKeep, saved, &w);
   carve(p, kN | kGrad, ws, &w);
-  return backward(p, x, d, w, st);
+  GdnMaps m;
+  return backward(p, x, d, false, m, w, st);
 }
 
 }  // namespace mlstm

@@ -25,6 +25,7 @@
 // (dbeta, dg).
 #pragma once
 
+#include "device_address.h"
 #include "gdn.h"
 #include "tc_ptx.cuh"
 
@@ -91,28 +92,71 @@ inline unsigned gdn_blocks(const GdnProblem& p, const GdnTcWs& w) {
   return (unsigned)(n < kGdnSms ? n : kGdnSms);
 }
 
+// Tensor maps of a call's arrays, encoded once for its launches: boxes of 64
+// columns and 128 rows (dq32, dk32: of 32 fp32 columns).
+struct GdnMaps {
+  CUtensorMap q, k, v, h, dh, dv, dq, dk;
+};
+
+// Lets a kernel use `smem` bytes in the current context (set once per context and
+// thread, a microsecond a time otherwise).
+cudaError_t gdn_allow_smem(const void* kern, size_t smem);
+
+// Launches a stage.  `after`: it may start while the stage before it in the
+// stream still runs (programmatic launch): its prologue and its loads of the
+// caller's arrays then overlap that stage's end, and gdn_wait_stage() below
+// orders the rest.  Saves 2 to 3 us between two short stages.
+template <class K, class... A>
+cudaError_t gdn_launch(K* kern, dim3 grid, int threads, size_t smem, bool after, cudaStream_t st,
+                       const A&... args) {
+  const cudaError_t e = gdn_allow_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // The stages, one launch each.
-cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
-                                  cudaStream_t st);
-cudaError_t launch_gdn_tc_mn(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
-                             cudaStream_t st);
+cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
+                                  const GdnTcWs& w, cudaStream_t st);
+cudaError_t launch_gdn_tc_mn(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
+                             const GdnTcWs& w, cudaStream_t st);
 // reverse: the gradient's recurrence, from dC_T (init) to dC0 (fin).
 cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* init, float* fin,
                                 const GdnTcWs& w, cudaStream_t st);
-// H may be null (y alone).
-cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, void* H, const GdnTcWs& w,
-                              cudaStream_t st);
-cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+// with_h: H, else y alone.
+cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
+                              bool with_h, const GdnTcWs& w, cudaStream_t st);
+// after: behind another stage (else first in its call).
+cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m, bool after,
                               const GdnTcWs& w, cudaStream_t st);
-cudaError_t launch_gdn_tc_dz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+cudaError_t launch_gdn_tc_dz(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
                              const GdnTcWs& w, cudaStream_t st);
 // With shared key heads a second launch adds dQ and dK over the value heads.
 cudaError_t launch_gdn_tc_grads(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
-                                const GdnTcWs& w, cudaStream_t st);
+                                const GdnMaps& m, const GdnTcWs& w, cudaStream_t st);
 
 namespace tc {
 
 constexpr uint32_t kBlk = 16384;  // bytes of a block: 128 rows x 64 columns of one term
+
+// Lets the next stage start its prologue; waits for the stage before (a no-op
+// without one).  What that stage wrote is read, and what it reads is written,
+// only behind the wait.
+__device__ __forceinline__ void gdn_next_stage() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void gdn_wait_stage() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // Operand descriptors: step kk of 16 along the product's inner axis.
 //   kmaj: rows are the outer axis, the inner axis runs along the columns

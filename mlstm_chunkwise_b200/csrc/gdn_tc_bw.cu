@@ -74,6 +74,7 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   };
 
   GdnItem x(blockIdx.x, p, w);
+  gdn_next_stage();
   if (lead) {
     for (int i = 0; i < 3; ++i) mbar_init(bar_qk + 8 * i, 1);
     fence_barrier_init();
@@ -84,9 +85,9 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     __syncwarp();
     tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
-  } else {
-    load_rows(x);
   }
+  gdn_wait_stage();
+  if (row) load_rows(x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -269,10 +270,11 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int slabs = (p.DK + 63) / 64;
   const long items = (long)p.BH * w.NC * ((w.nvt + 1) / 2);
   GdnRounds rd{bar_in + 16, 0u, true, Problem{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls}};
-  auto load_tiles = [&](const GdnItem& x) {
+  auto load_tiles = [&](const GdnItem& x, bool wait) {
     mbar_expect_tx(bar_in, slabs * (kBlk + x.tiles * 3 * 8192));
     const int kh = gdn_key_head(p, x.bh);
     for (int s = 0; s < slabs; ++s) tma_load_3d(ka + s * kBlk, &tm_k, s * 64, x.t0, kh, bar_in);
+    if (wait) gdn_wait_stage();
     for (int v = 0; v < x.tiles; ++v)
       for (int t = 0; t < 3; ++t)
         bulk_load(da + (2 * t + v) * kBlk, w.dS + ((x.cb * w.nvt + x.vt + v) * 3 + t) * kBlk,
@@ -295,18 +297,19 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
   };
 
   GdnItem x(blockIdx.x, p, w);
+  gdn_next_stage();
   if (lead) {
     for (int i = 0; i < 3; ++i) mbar_init(bar_in + 8 * i, 1);
     fence_barrier_init();
-    load_tiles(x);
+    load_tiles(x, true);
   }
   if (!row) {
     __syncwarp();
     tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
-  } else {
-    load_rows(x);
   }
+  gdn_wait_stage();
+  if (row) load_rows(x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -347,7 +350,7 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
         },
         gdn_nothing,
         [&] {
-          if (more) load_tiles(nx);
+          if (more) load_tiles(nx, false);
         });
     uint32_t v[32];
     if (row) {
@@ -523,16 +526,18 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
   if (lead) {
     for (int i = 0; i < 4; ++i) mbar_init(bar_a + 8 * i, 1);
     fence_barrier_init();
-    load_a(blockIdx.x, 0);
-    load_y(blockIdx.x, 0, bar_a);
   }
   if (!row) {
     __syncwarp();
     tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
-  } else {
-    load_rows(blockIdx.x);
   }
+  gdn_wait_stage();
+  if (lead) {
+    load_a(blockIdx.x, 0);
+    load_y(blockIdx.x, 0, bar_a);
+  }
+  if (row) load_rows(blockIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -905,58 +910,28 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 }  // namespace
 
-cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m, bool after,
                               const GdnTcWs& w, cudaStream_t st) {
-  CUtensorMap tq, tk, th;
-  const uint64_t kheads = (uint64_t)p.B * p.NHK;
-  if (!encode_tmap_bf16_3d(&tq, x.Q, p.DK, p.T, kheads, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, kheads, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&th, d.dH, p.DV, p.T, p.BH, 64, kGdnL))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(
-      gdn_tc_dz0_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kZSmem);
-  if (e != cudaSuccess) return e;
-  gdn_tc_dz0_kernel<<<gdn_blocks(p, w), kGdnThreads, kZSmem, st>>>(tq, tk, th, p, x.beta,
-                                                                              w);
-  return cudaGetLastError();
+  return gdn_launch(&gdn_tc_dz0_kernel, gdn_blocks(p, w), kGdnThreads, kZSmem, after, st, m.q, m.k,
+                    m.dh, p, x.beta, w);
 }
 
-cudaError_t launch_gdn_tc_dz(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
+cudaError_t launch_gdn_tc_dz(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
                              const GdnTcWs& w, cudaStream_t st) {
-  CUtensorMap tk, tv;
-  if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&tv, d.dV, p.DV, p.T, p.BH, 64, kGdnL))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(
-      gdn_tc_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kYSmem);
-  if (e != cudaSuccess) return e;
-  gdn_tc_dz_kernel<<<gdn_blocks(p, w), kGdnThreads, kYSmem, st>>>(
-      tk, tv, p, x.beta, w);
-  return cudaGetLastError();
+  return gdn_launch(&gdn_tc_dz_kernel, gdn_blocks(p, w), kGdnThreads, kYSmem, true, st, m.k, m.dv,
+                    p, x.beta, w);
 }
 
 cudaError_t launch_gdn_tc_grads(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
-                                const GdnTcWs& w, cudaStream_t st) {
-  CUtensorMap tq, tk, th, tdq, tdk;
-  const uint64_t kheads = (uint64_t)p.B * p.NHK;
-  const bool shared = w.dq != nullptr;
-  if (!encode_tmap_bf16_3d(&tq, x.Q, p.DK, p.T, kheads, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, kheads, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&th, d.dH, p.DV, p.T, p.BH, 64, kGdnL))
-    return cudaErrorInvalidValue;
-  if (shared ? !encode_tmap_3d(&tdq, w.dq, 4, p.DK, p.T, p.BH, 32, kGdnL, 128) ||
-                   !encode_tmap_3d(&tdk, w.dk, 4, p.DK, p.T, p.BH, 32, kGdnL, 128)
-             : !encode_tmap_bf16_3d(&tdq, d.dQ, p.DK, p.T, kheads, 64, kGdnL) ||
-                   !encode_tmap_bf16_3d(&tdk, d.dK, p.DK, p.T, kheads, 64, kGdnL))
-    return cudaErrorInvalidValue;
-  auto kern = shared ? gdn_tc_grads_kernel<true> : gdn_tc_grads_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
-  if (e != cudaSuccess) return e;
+                                const GdnMaps& m, const GdnTcWs& w, cudaStream_t st) {
   const long n = (long)p.BH * w.NC;
-  kern<<<(unsigned)(n < kGdnSms ? n : kGdnSms), kGdnThreads, kGSmem, st>>>(
-      tq, tk, th, tdq, tdk, p, x.beta, d.dg, d.dbeta, w);
-  if ((e = cudaGetLastError()) != cudaSuccess || !shared) return e;
-  return launch_gdn_group_sum(p, MLSTM_DT_BF16, w.dq, w.dk, d.dQ, d.dK, st);
+  auto go = [&](auto* kern) {
+    return gdn_launch(kern, (unsigned)(n < kGdnSms ? n : kGdnSms), kGdnThreads, kGSmem, true, st,
+                      m.q, m.k, m.dh, m.dq, m.dk, p, x.beta, d.dg, d.dbeta, w);
+  };
+  if (!w.dq) return go(&gdn_tc_grads_kernel<false>);
+  const cudaError_t e = go(&gdn_tc_grads_kernel<true>);
+  return e == cudaSuccess ? launch_gdn_group_sum(p, MLSTM_DT_BF16, w.dq, w.dk, d.dQ, d.dK, st) : e;
 }
 
 }  // namespace mlstm

@@ -49,6 +49,7 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
   const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
   auto chunk = [&](int i) { return (size_t)bh * NC + (kRev ? NC - 1 - i : i); };
 
+  gdn_next_stage();
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < kBars; ++i) mbar_init(bar(i), i == kSop ? kRows : 1);
     fence_barrier_init();
@@ -61,6 +62,7 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
+  gdn_wait_stage();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -171,12 +173,10 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
 
 cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* init, float* fin,
                                 const GdnTcWs& w, cudaStream_t st) {
-  auto kern = reverse ? gdn_tc_chain_kernel<true> : gdn_tc_chain_kernel<false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<dim3(w.nvt, p.BH), kThreads, kSmem, st>>>(p, init, fin, w);
-  return cudaGetLastError();
+  const dim3 grid(w.nvt, p.BH);
+  if (reverse)
+    return gdn_launch(&gdn_tc_chain_kernel<true>, grid, kThreads, kSmem, true, st, p, init, fin, w);
+  return gdn_launch(&gdn_tc_chain_kernel<false>, grid, kThreads, kSmem, true, st, p, init, fin, w);
 }
 
 }  // namespace mlstm

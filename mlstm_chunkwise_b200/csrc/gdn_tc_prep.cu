@@ -49,6 +49,7 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
   const size_t cb = (size_t)bh * w.NC + c;
   const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
 
+  gdn_next_stage();
   if (tid == 0) {
     mbar_init(bar_k, 1);
     mbar_init(bar, 1);
@@ -318,6 +319,7 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   };
 
   GdnItem x(blockIdx.x, p, w);
+  gdn_next_stage();
   if (lead) {
     for (int i = 0; i < 3; ++i) mbar_init(bar_k + 8 * i, 1);
     fence_barrier_init();
@@ -328,7 +330,9 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __syncwarp();
     tmem_alloc(smem_u32((const void*)slot), 512);
     tmem_relinquish();
-  } else {
+  }
+  gdn_wait_stage();
+  if (row) {
     load_rows(x);
     if (h == 0) slam[r] = gdn_exp(ngc);
   }
@@ -468,30 +472,20 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
 }  // namespace
 
-cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
-                                  cudaStream_t st) {
-  CUtensorMap tk;
-  if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL))
-    return cudaErrorInvalidValue;
-  auto kern = w.tinvt ? gdn_tc_inverse_kernel<true> : gdn_tc_inverse_kernel<false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kISmem);
-  if (e != cudaSuccess) return e;
-  kern<<<dim3(w.NC, p.BH), kInvThreads, kISmem, st>>>(tk, p, x.g, x.beta, w);
-  return cudaGetLastError();
+cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
+                                  const GdnTcWs& w, cudaStream_t st) {
+  const dim3 grid(w.NC, p.BH);
+  if (w.tinvt)
+    return gdn_launch(&gdn_tc_inverse_kernel<true>, grid, kInvThreads, kISmem, false, st, m.k, p,
+                      x.g, x.beta, w);
+  return gdn_launch(&gdn_tc_inverse_kernel<false>, grid, kInvThreads, kISmem, false, st, m.k, p,
+                    x.g, x.beta, w);
 }
 
-cudaError_t launch_gdn_tc_mn(const GdnProblem& p, const GdnInputs& x, const GdnTcWs& w,
-                             cudaStream_t st) {
-  CUtensorMap tk, tv;
-  if (!encode_tmap_bf16_3d(&tk, x.K, p.DK, p.T, (uint64_t)p.B * p.NHK, 64, kGdnL) ||
-      !encode_tmap_bf16_3d(&tv, x.V, p.DV, p.T, p.BH, 64, kGdnL))
-    return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(
-      gdn_tc_mn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMSmem);
-  if (e != cudaSuccess) return e;
-  gdn_tc_mn_kernel<<<gdn_blocks(p, w), kGdnThreads, kMSmem, st>>>(tk, tv, p, x.beta, w);
-  return cudaGetLastError();
+cudaError_t launch_gdn_tc_mn(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
+                             const GdnTcWs& w, cudaStream_t st) {
+  return gdn_launch(&gdn_tc_mn_kernel, gdn_blocks(p, w), kGdnThreads, kMSmem, true, st, m.k, m.v, p,
+                    x.beta, w);
 }
 
 }  // namespace mlstm
