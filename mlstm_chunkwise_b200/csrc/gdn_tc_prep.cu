@@ -26,8 +26,8 @@ constexpr uint32_t kBi = 8192;              // lo term of the products' images (
 constexpr uint32_t kIDiag = kBlk;           // float[4][32][kLd]
 constexpr uint32_t kIGc = 4 * kBlk;
 constexpr uint32_t kIBeta = kIGc + 1024;
-constexpr uint32_t kICol = kIBeta + 512;    // beta times the column's factor
-constexpr uint32_t kIBar = kICol + 512;
+constexpr uint32_t kICol = kIBeta + 512;    // float[2][128]: beta times the column's factor
+constexpr uint32_t kIBar = kICol + 1024;
 constexpr uint32_t kISmem = kIBar + 64;
 
 // kT: also Tinv^T.
@@ -74,7 +74,10 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
   const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
   bool ok = true;
   uint32_t phase = 0;
-  if (warp >= 4) scol[r] = sbeta[r] * gdn_col_factor(gc[r], 31);
+  if (warp >= 4) {
+    scol[r] = sbeta[r] * gdn_col_factor(gc[r], 31);
+    scol[128 + r] = __fdividef(sbeta[r], gdn_col_factor(gc[r], 0));
+  }
 
   run_mma(bar, phase, ok, wt, 0x42, [&] {
     ok = mbar_wait(bar_k, 0, wt, 0x41);
@@ -102,11 +105,19 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
     uint32_t v[32];
     tmem_ld32(trow + q * 32, v);
     tmem_wait_ld();
+    if (gc[q * 32].x - gc[q * 32 + 31].x > kGdnFlat) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int s = q * 32 + e;
-      dq[e * kLd + lane] =
-          e < lane ? gdn_decay(gr, gc[s]) * sbeta[s] * __uint_as_float(v[e]) : 0.f;
+      for (int e = 0; e < 32; ++e) {
+        const int s = q * 32 + e;
+        dq[e * kLd + lane] =
+            e < lane ? gdn_decay(gr, gc[s]) * sbeta[s] * __uint_as_float(v[e]) : 0.f;
+      }
+    } else {
+      const float f = gdn_decay(gr, gc[q * 32]);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        dq[e * kLd + lane] =
+            e < lane ? f * scol[128 + q * 32 + e] * __uint_as_float(v[e]) : 0.f;
     }
   } else if (q & 1) {
     a_block(q - 1, hi0, lo0);
