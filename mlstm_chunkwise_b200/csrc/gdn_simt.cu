@@ -22,19 +22,39 @@ __host__ __device__ inline int chunks_of(int T) { return (T + kL - 1) / kL; }
 template <int TN, bool AK, bool BK, class FA, class FB>
 __device__ __forceinline__ void block_mm(float (&acc)[4][TN], int K, FA a, FB b, float* sa,
                                          float* sb) {
-  constexpr int N = 16 * TN;
+  constexpr int N = 16 * TN, kA = 64 * kKB / kThreads, kB = N * kKB / kThreads;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  // a slab's elements are loaded together, while the slab before is worked on:
+  // one by one, their latency made the recurrence four times slower
+  float ra[kA], rb[kB];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < kA; ++u) {
+      const int i = tid + u * kThreads, m = AK ? i / kKB : i % 64, k = AK ? i % kKB : i / 64;
+      ra[u] = k0 + k < K ? a(m, k0 + k) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kB; ++u) {
+      const int i = tid + u * kThreads, n = BK ? i / kKB : i % N, k = BK ? i % kKB : i / N;
+      rb[u] = k0 + k < K ? b(k0 + k, n) : 0.f;
+    }
+  };
+  __syncthreads();
+  load(0);
   for (int k0 = 0; k0 < K; k0 += kKB) {
-    __syncthreads();
-    for (int i = tid; i < 64 * kKB; i += kThreads) {
-      const int m = AK ? i / kKB : i % 64, k = AK ? i % kKB : i / 64;
-      sa[k * 68 + m] = k0 + k < K ? a(m, k0 + k) : 0.f;
+    if (k0) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kA; ++u) {
+      const int i = tid + u * kThreads, m = AK ? i / kKB : i % 64, k = AK ? i % kKB : i / 64;
+      sa[k * 68 + m] = ra[u];
     }
-    for (int i = tid; i < N * kKB; i += kThreads) {
-      const int n = BK ? i / kKB : i % N, k = BK ? i % kKB : i / N;
-      sb[k * (N + 4) + n] = k0 + k < K ? b(k0 + k, n) : 0.f;
+#pragma unroll
+    for (int u = 0; u < kB; ++u) {
+      const int i = tid + u * kThreads, n = BK ? i / kKB : i % N, k = BK ? i % kKB : i / N;
+      sb[k * (N + 4) + n] = rb[u];
     }
     __syncthreads();
+    if (k0 + kKB < K) load(k0 + kKB);
 #pragma unroll 8
     for (int k = 0; k < kKB; ++k) {
       const float4 av = *reinterpret_cast<const float4*>(sa + k * 68 + ty * 4);
@@ -158,15 +178,46 @@ gdn_simt_prep(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
       sA[r * 65 + s] = s < r ? gam(sgc[r], sgc[s]) * sbeta[s] * acc[i][j] : 0.f;
     }
   __syncthreads();
-  // column j of the inverse by forward substitution, one thread per column;
-  // x_r overwrites the (unused) upper triangle's transposed place sX[j][r]
+  // the inverse, sX[column][row]: the two 32 x 32 diagonal blocks by forward
+  // substitution (a warp each, a lane per column: once x_s is known its multiples
+  // leave all later rows, independent products), then -T22 A21 T11
   float* sX = sa;  // [64][65], over both slabs
   if (tid < kL) {
-    for (int r = 0; r < kL; ++r) {
-      float x = r == tid ? 1.f : 0.f;
-      for (int s = tid; s < r; ++s) x = fmaf(-sA[r * 65 + s], sX[tid * 65 + s], x);
-      sX[tid * 65 + r] = r < tid ? 0.f : x;
+    const int b0 = tid & 32, c = tid & 31;
+    float x[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r) x[r] = r == c ? 1.f : 0.f;
+#pragma unroll
+    for (int k = 0; k < 31; ++k)
+#pragma unroll
+      for (int r = k + 1; r < 32; ++r) x[r] = fmaf(-sA[(b0 + r) * 65 + b0 + k], x[k], x[r]);
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      sX[tid * 65 + b0 + r] = x[r];
+      if (b0) sX[tid * 65 + r] = 0.f;  // above the diagonal
     }
+  }
+  __syncthreads();
+  {
+    const int c = tid & 31, r0 = tid >> 5;
+    float x[4] = {};
+    for (int k = 0; k < 32; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = fmaf(sA[(32 + r0 + 8 * i) * 65 + k], sX[c * 65 + k], x[i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sA[(32 + r0 + 8 * i) * 65 + c] = x[i];
+      x[i] = 0.f;
+    }
+    __syncthreads();
+    for (int k = 0; k < 32; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = fmaf(-sX[(32 + k) * 65 + 32 + r0 + 8 * i], sA[(32 + k) * 65 + c], x[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sX[c * 65 + 32 + r0 + 8 * i] = x[i];
   }
   __syncthreads();
   for (int i = tid; i < kL * kL; i += kThreads)
