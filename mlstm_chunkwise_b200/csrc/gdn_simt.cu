@@ -83,14 +83,16 @@ __device__ __forceinline__ void zero(float (&acc)[4][TN]) {
 
 constexpr int kSa = kKB * 68, kSb = kKB * 68;  // floats of the two staged slabs
 
-// Workspace pieces (fp32): per (bh, chunk) Tinv and Gam . QK^T (without beta)
-// [64][64], gc as (hi, lo) pairs per token; the backward adds y, dz
-// [BH][NC * 64][DV], the states entering and the state gradients leaving every
-// chunk [BH][NC][DK][DV], and with shared key heads dq, dk [BH][T][DK].
+// Workspace pieces (fp32), per (bh, chunk): Tinv and Gam . QK^T (without beta)
+// [64][64], gc as (hi, lo) pairs per token; W = Tinv Lam K [64][DK]; y [64][DV],
+// in its place first U = Tinv V; S [DK][DV], the state entering.  The backward
+// adds E = Tinv^T beta D K [64][DK]; dz [64][DV], first dz without its part from
+// dS'; dS [DK][DV], the state gradient leaving, first Q^T (scale Lam dH); and with
+// shared key heads dq, dk [BH][T][DK].
 struct Ws {
   float *tinv, *p;
   float2* gc;
-  float *y, *dz, *S, *dS, *dq, *dk;
+  float *W, *y, *S, *E, *dz, *dS, *dq, *dk;
   size_t bytes;
 };
 Ws layout(const GdnProblem& p, bool bw, char* base) {
@@ -105,10 +107,12 @@ Ws layout(const GdnProblem& p, bool bw, char* base) {
   w.tinv = take(nc * kL * kL);
   w.p = take(nc * kL * kL);
   w.gc = reinterpret_cast<float2*>(take(nc * kL * 2));
+  w.W = take(nc * kL * p.DK);
+  w.y = take(nc * kL * p.DV);
+  w.S = take(nc * p.DK * p.DV);
   if (bw) {
-    w.y = take(nc * kL * p.DV);
+    w.E = take(nc * kL * p.DK);
     w.dz = take(nc * kL * p.DV);
-    w.S = take(nc * p.DK * p.DV);
     w.dS = take(nc * p.DK * p.DV);
     if (p.group > 1) {
       w.dq = take((size_t)p.BH * p.T * p.DK);
@@ -126,7 +130,7 @@ __device__ __forceinline__ float gam(float2 r, float2 s) {
 
 // ---- per chunk: gc, Tinv, Gam . QK^T -----------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 gdn_simt_prep(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
               const float* __restrict__ g, const float* __restrict__ beta, Ws w) {
   extern __shared__ float sh[];
@@ -224,216 +228,219 @@ gdn_simt_prep(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
     w.tinv[cb * kL * kL + i] = sX[(i % kL) * 65 + i / kL];
 }
 
-// ---- forward recurrence: one CTA per (bh, 32 value columns) ------------
-// With kOut it also writes H; with w.S it keeps y and the entering states.
-template <typename T, bool kOut>
-__global__ void __launch_bounds__(kThreads)
-gdn_simt_chain(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
+// Gates of a chunk: gc, and per token Lam, D and beta.
+struct Gates64 {
+  float2 gc[kL];
+  float lam[kL], d[kL], beta[kL];
+};
+__device__ __forceinline__ void load_gates(Gates64* g, const GdnProblem& p, const Ws& w, size_t cb,
+                                           const float* beta, long at, int n) {
+  const int t = threadIdx.x;
+  if (t < kL) {
+    const float2 x = w.gc[cb * kL + t];
+    g->gc[t] = x;
+    g->lam[t] = expf(x.x + x.y);
+    g->d[t] = gam(w.gc[cb * kL + kL - 1], x);
+    g->beta[t] = t < n ? beta[at + t] : 0.f;
+  }
+  __syncthreads();
+}
+// Rows of Q, K (or V, dH) of a chunk; zero outside.
+template <typename T>
+struct Rows {
+  const T* p;
+  int n, cols;
+  __device__ float operator()(int r, int c) const {
+    return r < n && c < cols ? to_float(p[(long)r * cols + c]) : 0.f;
+  }
+};
+
+// ---- per chunk: W and U; for the backward E, dz0 and Q^T (scale Lam dH) ------
+template <typename T, bool kBw>
+__global__ void __launch_bounds__(kThreads, 2)
+gdn_simt_chunk(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
                const T* __restrict__ V, const float* __restrict__ beta,
-               const float* __restrict__ C0, T* __restrict__ H, float* __restrict__ C_T, Ws w) {
+               const T* __restrict__ dH, Ws w) {
   extern __shared__ float sh[];
-  float *sa = sh, *sb = sa + kSa, *sz = sb + kSb;  // sz, sy [64][33]
-  float *sy = sz + 64 * 33, *sS = sy + 64 * 33;    // sS [DK][33]
-  float2* sgc = reinterpret_cast<float2*>(sS + p.DK * 33 + (p.DK & 1));
-  float* sbeta = reinterpret_cast<float*>(sgc + 64);
+  float *sa = sh, *sb = sa + kSa, *sw = sb + kSb;  // sw [64][65]
+  Gates64* g = reinterpret_cast<Gates64*>(sw + 64 * 66);
+  const int c = blockIdx.x, bh = blockIdx.y, NC = gridDim.x;
+  const int t0 = c * kL, n = min(kL, p.T - t0);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const size_t cb = (size_t)bh * NC + c;
+  const long kh = gdn_key_head(p, bh), at = (long)bh * p.T + t0;
+  load_gates(g, p, w, cb, beta, at, n);
+  const Rows<T> q{Q + (kh * p.T + t0) * p.DK, n, p.DK}, k{K + (kh * p.T + t0) * p.DK, n, p.DK};
+  const float* tinv = w.tinv + cb * kL * kL;
+  float acc[4][4];
+  auto put = [&](float* dst, int rows, int cols, int r0, int c0) {
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j) {
+        const int r = r0 + ty * 4 + i, cc = c0 + tx * 4 + j;
+        if (r < rows && cc < cols) dst[(long)r * cols + cc] = acc[i][j];
+      }
+  };
+  for (int d0 = 0; d0 < p.DK; d0 += 64) {
+    zero(acc);
+    block_mm<4, true, false>(
+        acc, kL, [&](int m, int s) { return tinv[m * kL + s] * g->lam[s]; },
+        [&](int s, int d) { return k(s, d0 + d); }, sa, sb);
+    put(w.W + cb * kL * p.DK, kL, p.DK, 0, d0);
+    if (kBw) {
+      zero(acc);
+      block_mm<4, false, false>(
+          acc, kL, [&](int m, int s) { return tinv[s * kL + m] * (g->beta[s] * g->d[s]); },
+          [&](int s, int d) { return k(s, d0 + d); }, sa, sb);
+      put(w.E + cb * kL * p.DK, kL, p.DK, 0, d0);
+    }
+  }
+  const Rows<T> v{V + at * p.DV, n, p.DV};
+  for (int v0 = 0; v0 < p.DV; v0 += 64) {
+    zero(acc);
+    block_mm<4, true, false>(
+        acc, kL, [&](int m, int s) { return tinv[m * kL + s]; },
+        [&](int s, int e) { return v(s, v0 + e); }, sa, sb);
+    put(w.y + cb * kL * p.DV, kL, p.DV, 0, v0);
+    if (!kBw) continue;
+    const Rows<T> dh{dH + at * p.DV, n, p.DV};
+    zero(acc);
+    block_mm<4, false, false>(
+        acc, kL, [&](int m, int s) { return w.p[cb * kL * kL + s * kL + m]; },
+        [&](int s, int e) { return dh(s, v0 + e); }, sa, sb);
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j)
+        sw[(ty * 4 + i) * 65 + tx * 4 + j] = p.scale * g->beta[ty * 4 + i] * acc[i][j];
+    zero(acc);
+    block_mm<4, false, false>(
+        acc, kL, [&](int m, int s) { return tinv[s * kL + m]; },
+        [&](int s, int e) { return sw[s * 65 + e]; }, sa, sb);
+    put(w.dz + cb * kL * p.DV, kL, p.DV, 0, v0);
+    for (int d0 = 0; d0 < p.DK; d0 += 64) {
+      zero(acc);
+      block_mm<4, false, false>(
+          acc, kL, [&](int m, int s) { return q(s, d0 + m) * (p.scale * g->lam[s]); },
+          [&](int s, int e) { return dh(s, v0 + e); }, sa, sb);
+      put(w.dS + cb * p.DK * p.DV, p.DK, p.DV, d0, v0);
+    }
+  }
+}
+
+// ---- the recurrences: one CTA per (bh, 32 value columns) ----------------
+// Forward: y = U - W S, S' = e^G S + K^T (D beta y).  Reverse: dz = dz0 + E dS',
+// dS = e^G dS' + Q^T (scale Lam dH) - K^T (Lam dz).
+template <typename T, bool kRev>
+__global__ void __launch_bounds__(kThreads)
+gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ beta,
+               const float* __restrict__ init, float* __restrict__ fin, T* __restrict__ dV, Ws w) {
+  extern __shared__ float sh[];
+  float *sa = sh, *sb = sa + kSa, *sy = sb + kSb;  // sy [64][33]
+  float* sS = sy + 64 * 33;                        // [DK][33]
+  Gates64* g = reinterpret_cast<Gates64*>(sS + p.DK * 33 + (p.DK & 1));
   const int v0 = blockIdx.x * kVT, bh = blockIdx.y, NC = chunks_of(p.T);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const long kh = gdn_key_head(p, bh);
   for (int i = tid; i < p.DK * kVT; i += kThreads) {
     const int d = i / kVT, v = i % kVT;
-    sS[d * 33 + v] =
-        C0 && v0 + v < p.DV ? C0[((long)bh * p.DK + d) * p.DV + v0 + v] : 0.f;
+    sS[d * 33 + v] = init && v0 + v < p.DV ? init[((long)bh * p.DK + d) * p.DV + v0 + v] : 0.f;
   }
-  for (int c = 0; c < NC; ++c) {
-    const int t0 = c * kL, n = min(kL, p.T - t0);
+  const float* A = kRev ? w.E : w.W;
+  float *Y = kRev ? w.dz : w.y, *St = kRev ? w.dS : w.S;
+  for (int step = 0; step < NC; ++step) {
+    const int c = kRev ? NC - 1 - step : step, t0 = c * kL, n = min(kL, p.T - t0);
     const size_t cb = (size_t)bh * NC + c;
-    const T* Kp = K + (kh * p.T + t0) * p.DK;
-    const T* Qp = Q + (kh * p.T + t0) * p.DK;
     __syncthreads();
-    if (tid < kL) {
-      sgc[tid] = w.gc[cb * kL + tid];
-      sbeta[tid] = tid < n ? beta[(long)bh * p.T + t0 + tid] : 0.f;
-    }
-    if (w.S)
-      for (int i = tid; i < p.DK * kVT; i += kThreads) {
-        const int d = i / kVT, v = i % kVT;
-        if (v0 + v < p.DV) w.S[(cb * p.DK + d) * p.DV + v0 + v] = sS[d * 33 + v];
-      }
-    __syncthreads();
-    auto krow = [&](int m, int k) { return m < n ? to_float(Kp[(long)m * p.DK + k]) : 0.f; };
-    auto st = [&](int k, int v) { return sS[k * 33 + v]; };
-    float acc[4][2], oacc[4][2];
-    zero(acc);
-    block_mm<2, true, false>(acc, p.DK, krow, st, sa, sb);
+    load_gates(g, p, w, cb, beta, (long)bh * p.T + t0, n);
+    const Rows<T> k{K + (kh * p.T + t0) * p.DK, n, p.DK};
+    float acc[4][2], add[4][2];
+    // what a product's result is added to is loaded ahead of the product
     for (int i = 0; i < 4; ++i)
       for (int j = 0; j < 2; ++j) {
-        const int r = ty * 4 + i, v = tx * 2 + j;
-        const float vv = r < n && v0 + v < p.DV
-                             ? to_float(V[((long)bh * p.T + t0 + r) * p.DV + v0 + v])
-                             : 0.f;
-        sz[r * 33 + v] = vv - expf(sgc[r].x + sgc[r].y) * acc[i][j];
+        const int r = ty * 4 + i, v = v0 + tx * 2 + j;
+        add[i][j] = v < p.DV ? Y[(cb * kL + r) * p.DV + v] : 0.f;
       }
-    __syncthreads();
     zero(acc);
     block_mm<2, true, false>(
-        acc, kL, [&](int m, int k) { return w.tinv[cb * kL * kL + m * kL + k]; },
-        [&](int k, int v) { return sz[k * 33 + v]; }, sa, sb);
+        acc, p.DK, [&](int m, int d) { return A[(cb * kL + m) * p.DK + d]; },
+        [&](int d, int v) { return sS[d * 33 + v]; }, sa, sb);
     for (int i = 0; i < 4; ++i)
       for (int j = 0; j < 2; ++j) {
         const int r = ty * 4 + i, v = tx * 2 + j;
-        sy[r * 33 + v] = sbeta[r] * acc[i][j];
-        if (w.S && v0 + v < p.DV) w.y[(cb * kL + r) * p.DV + v0 + v] = acc[i][j];
+        const float y = kRev ? add[i][j] + acc[i][j] : add[i][j] - acc[i][j];
+        if (v0 + v < p.DV) {
+          Y[(cb * kL + r) * p.DV + v0 + v] = y;
+          if (kRev && r < n) dV[((long)bh * p.T + t0 + r) * p.DV + v0 + v] = from_float<T>(y);
+        }
+        sy[r * 33 + v] = y * (kRev ? -g->lam[r] : g->d[r] * g->beta[r]);
       }
     __syncthreads();
-    if (kOut) {
-      zero(oacc);
-      block_mm<2, true, false>(
-          oacc, p.DK, [&](int m, int k) { return m < n ? to_float(Qp[(long)m * p.DK + k]) : 0.f; },
-          st, sa, sb);
-      for (int i = 0; i < 4; ++i) {
-        const float2 gr = sgc[ty * 4 + i];
-        for (int j = 0; j < 2; ++j) oacc[i][j] *= expf(gr.x + gr.y);
-      }
-      block_mm<2, true, false>(
-          oacc, kL, [&](int m, int k) { return w.p[cb * kL * kL + m * kL + k]; },
-          [&](int k, int v) { return sy[k * 33 + v]; }, sa, sb);
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 2; ++j) {
-          const int r = ty * 4 + i, v = v0 + tx * 2 + j;
-          if (r < n && v < p.DV)
-            H[((long)bh * p.T + t0 + r) * p.DV + v] = from_float<T>(p.scale * oacc[i][j]);
-        }
-    }
-    // S' = e^G S + K^T (D beta y), 64 state rows at a time (each product ends
-    // with a barrier, and only this CTA's own rows are written)
-    const float2 gl = sgc[kL - 1];
+    const float2 gl = g->gc[kL - 1];
     const float eg = expf(gl.x + gl.y);
+    // 64 state rows at a time; a thread keeps the rows that it updates
     for (int d0 = 0; d0 < p.DK; d0 += 64) {
+      if (kRev)
+        for (int i = 0; i < 4; ++i)
+          for (int j = 0; j < 2; ++j) {
+            const int d = d0 + ty * 4 + i, v = v0 + tx * 2 + j;
+            add[i][j] = d < p.DK && v < p.DV ? St[(cb * p.DK + d) * p.DV + v] : 0.f;
+          }
       zero(acc);
       block_mm<2, false, false>(
-          acc, kL,
-          [&](int m, int k) {
-            return k < n && d0 + m < p.DK ? to_float(Kp[(long)k * p.DK + d0 + m]) : 0.f;
-          },
-          [&](int k, int v) { return gam(gl, sgc[k]) * sy[k * 33 + v]; }, sa, sb);
+          acc, kL, [&](int m, int s) { return k(s, d0 + m); },
+          [&](int s, int v) { return sy[s * 33 + v]; }, sa, sb);
       for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 2; ++j) {
           const int d = d0 + ty * 4 + i, v = tx * 2 + j;
-          if (d < p.DK) sS[d * 33 + v] = fmaf(eg, sS[d * 33 + v], acc[i][j]);
+          if (d >= p.DK) continue;
+          const float old = sS[d * 33 + v];
+          if (v0 + v < p.DV) St[(cb * p.DK + d) * p.DV + v0 + v] = old;
+          sS[d * 33 + v] = fmaf(eg, old, kRev ? acc[i][j] + add[i][j] : acc[i][j]);
         }
     }
   }
   __syncthreads();
-  if (C_T)
+  if (fin)
     for (int i = tid; i < p.DK * kVT; i += kThreads) {
       const int d = i / kVT, v = i % kVT;
-      if (v0 + v < p.DV) C_T[((long)bh * p.DK + d) * p.DV + v0 + v] = sS[d * 33 + v];
+      if (v0 + v < p.DV) fin[((long)bh * p.DK + d) * p.DV + v0 + v] = sS[d * 33 + v];
     }
 }
 
-// ---- reverse recurrence: dz (= dV) and the state gradients --------------
+// ---- per chunk, 64 value columns: H = scale (Lam Q S + P beta y) --------
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-gdn_simt_bchain(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
-                const float* __restrict__ beta, const T* __restrict__ dH,
-                const float* __restrict__ dC_T, T* __restrict__ dV, float* __restrict__ dC0, Ws w) {
+__global__ void __launch_bounds__(kThreads, 2)
+gdn_simt_out(GdnProblem p, const T* __restrict__ Q, const float* __restrict__ beta,
+             T* __restrict__ H, Ws w) {
   extern __shared__ float sh[];
-  float *sa = sh, *sb = sa + kSa, *sw = sb + kSb;  // sw, sd [64][33]
-  float *sd = sw + 64 * 33, *sS = sd + 64 * 33;    // sS [DK][33]: the state gradient
-  float2* sgc = reinterpret_cast<float2*>(sS + p.DK * 33 + (p.DK & 1));
-  float* sbeta = reinterpret_cast<float*>(sgc + 64);
-  const int v0 = blockIdx.x * kVT, bh = blockIdx.y, NC = chunks_of(p.T);
+  float *sa = sh, *sb = sa + kSa;
+  Gates64* g = reinterpret_cast<Gates64*>(sb + kSb);
+  const int v0 = blockIdx.x * 64, c = blockIdx.y, bh = blockIdx.z, NC = gridDim.y;
+  const int t0 = c * kL, n = min(kL, p.T - t0);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const long kh = gdn_key_head(p, bh);
-  for (int i = tid; i < p.DK * kVT; i += kThreads) {
-    const int d = i / kVT, v = i % kVT;
-    sS[d * 33 + v] =
-        dC_T && v0 + v < p.DV ? dC_T[((long)bh * p.DK + d) * p.DV + v0 + v] : 0.f;
-  }
-  for (int c = NC - 1; c >= 0; --c) {
-    const int t0 = c * kL, n = min(kL, p.T - t0);
-    const size_t cb = (size_t)bh * NC + c;
-    const T* Kp = K + (kh * p.T + t0) * p.DK;
-    const T* Qp = Q + (kh * p.T + t0) * p.DK;
-    __syncthreads();
-    if (tid < kL) {
-      sgc[tid] = w.gc[cb * kL + tid];
-      sbeta[tid] = tid < n ? beta[(long)bh * p.T + t0 + tid] : 0.f;
-    }
-    for (int i = tid; i < p.DK * kVT; i += kThreads) {
-      const int d = i / kVT, v = i % kVT;
-      if (v0 + v < p.DV) w.dS[(cb * p.DK + d) * p.DV + v0 + v] = sS[d * 33 + v];
-    }
-    for (int i = tid; i < kL * kVT; i += kThreads) {
-      const int r = i / kVT, v = i % kVT;
-      sd[r * 33 + v] = r < n && v0 + v < p.DV
-                           ? to_float(dH[((long)bh * p.T + t0 + r) * p.DV + v0 + v])
-                           : 0.f;
-    }
-    __syncthreads();
-    const float2 gl = sgc[kL - 1];
-    float acc[4][2], acc2[4][2];
-    zero(acc);
-    zero(acc2);
-    block_mm<2, false, false>(
-        acc, kL, [&](int m, int k) { return w.p[cb * kL * kL + k * kL + m]; },
-        [&](int k, int v) { return sd[k * 33 + v]; }, sa, sb);
-    block_mm<2, true, false>(
-        acc2, p.DK, [&](int m, int k) { return m < n ? to_float(Kp[(long)m * p.DK + k]) : 0.f; },
-        [&](int k, int v) { return sS[k * 33 + v]; }, sa, sb);
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 2; ++j) {
-        const int r = ty * 4 + i;
-        sw[r * 33 + tx * 2 + j] =
-            sbeta[r] * fmaf(p.scale, acc[i][j], gam(gl, sgc[r]) * acc2[i][j]);
-      }
-    __syncthreads();
-    zero(acc);
-    block_mm<2, false, false>(
-        acc, kL, [&](int m, int k) { return w.tinv[cb * kL * kL + k * kL + m]; },
-        [&](int k, int v) { return sw[k * 33 + v]; }, sa, sb);
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 2; ++j) {
-        const int r = ty * 4 + i, v = tx * 2 + j;
-        if (v0 + v < p.DV) {
-          w.dz[(cb * kL + r) * p.DV + v0 + v] = acc[i][j];
-          if (r < n) dV[((long)bh * p.T + t0 + r) * p.DV + v0 + v] = from_float<T>(acc[i][j]);
-        }
-        const float lam = expf(sgc[r].x + sgc[r].y);
-        sw[r * 33 + v] = -lam * acc[i][j];
-        sd[r * 33 + v] *= p.scale * lam;
-      }
-    __syncthreads();
-    const float eg = expf(gl.x + gl.y);
-    for (int d0 = 0; d0 < p.DK; d0 += 64) {
-      auto col = [&](const T* P) {
-        return [=](int m, int k) {
-          return k < n && d0 + m < p.DK ? to_float(P[(long)k * p.DK + d0 + m]) : 0.f;
-        };
-      };
-      zero(acc);
-      block_mm<2, false, false>(acc, kL, col(Kp), [&](int k, int v) { return sw[k * 33 + v]; }, sa,
-                                sb);
-      block_mm<2, false, false>(acc, kL, col(Qp), [&](int k, int v) { return sd[k * 33 + v]; }, sa,
-                                sb);
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 2; ++j) {
-          const int d = d0 + ty * 4 + i, v = tx * 2 + j;
-          if (d < p.DK) sS[d * 33 + v] = fmaf(eg, sS[d * 33 + v], acc[i][j]);
-        }
-    }
-  }
-  __syncthreads();
-  if (dC0)
-    for (int i = tid; i < p.DK * kVT; i += kThreads) {
-      const int d = i / kVT, v = i % kVT;
-      if (v0 + v < p.DV) dC0[((long)bh * p.DK + d) * p.DV + v0 + v] = sS[d * 33 + v];
+  const size_t cb = (size_t)bh * NC + c;
+  const long kh = gdn_key_head(p, bh), at = (long)bh * p.T + t0;
+  load_gates(g, p, w, cb, beta, at, n);
+  const Rows<T> q{Q + (kh * p.T + t0) * p.DK, n, p.DK};
+  const Rows<float> s{w.S + cb * p.DK * p.DV, p.DK, p.DV}, y{w.y + cb * kL * p.DV, kL, p.DV};
+  float acc[4][4];
+  zero(acc);
+  block_mm<4, true, false>(
+      acc, p.DK, [&](int m, int d) { return q(m, d); },
+      [&](int d, int v) { return s(d, v0 + v); }, sa, sb);
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) acc[i][j] *= g->lam[ty * 4 + i];
+  block_mm<4, true, false>(
+      acc, kL, [&](int m, int t) { return w.p[cb * kL * kL + m * kL + t]; },
+      [&](int t, int v) { return g->beta[t] * y(t, v0 + v); }, sa, sb);
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) {
+      const int r = ty * 4 + i, v = v0 + tx * 4 + j;
+      if (r < n && v < p.DV) H[(at + r) * p.DV + v] = from_float<T>(p.scale * acc[i][j]);
     }
 }
 
 // ---- per chunk: dQ, dK, dg, dbeta ---------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 gdn_simt_grads(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
                const float* __restrict__ beta, const T* __restrict__ dH, T* __restrict__ dQ,
                T* __restrict__ dK, float* __restrict__ dg, float* __restrict__ dbeta, Ws w) {
@@ -656,9 +663,11 @@ __global__ void gdn_group_sum(GdnProblem p, const float* __restrict__ dq,
 }
 
 size_t chain_smem(const GdnProblem& p) {
-  return (size_t)(kSa + kSb + 2 * 64 * 33 + p.DK * 33 + (p.DK & 1) + 64 * 3) * 4;
+  return (size_t)(kSa + kSb + 64 * 33 + p.DK * 33 + (p.DK & 1)) * 4 + sizeof(Gates64);
 }
 constexpr size_t kPrepSmem = (kSa + kSb + 64 * 66 + 64 * 3) * 4;
+constexpr size_t kChunkSmem = (kSa + kSb + 64 * 66) * 4 + sizeof(Gates64);
+constexpr size_t kOutSmem = (kSa + kSb) * 4 + sizeof(Gates64);
 constexpr size_t kGradSmem = (kSa + kSb + 2 * 64 * 65 + 5 * 64 + 64 * 17 + 64 + 128) * 4;
 
 template <class F>
@@ -675,18 +684,31 @@ cudaError_t prep(const GdnProblem& p, const GdnInputs& x, const Ws& w, cudaStrea
   return cudaGetLastError();
 }
 
+// prep and chunk quantities, then the forward recurrence
+template <typename T, bool kBw>
+cudaError_t states(const GdnProblem& p, const GdnInputs& x, const void* dH, float* C_T, const Ws& w,
+                   cudaStream_t st) {
+  cudaError_t e = prep<T>(p, x, w, st);
+  if (e != cudaSuccess) return e;
+  if ((e = allow(gdn_simt_chunk<T, kBw>, kChunkSmem)) != cudaSuccess) return e;
+  gdn_simt_chunk<T, kBw><<<dim3(chunks_of(p.T), p.BH), kThreads, kChunkSmem, st>>>(
+      p, (const T*)x.Q, (const T*)x.K, (const T*)x.V, x.beta, (const T*)dH, w);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = allow(gdn_simt_chain<T, false>, chain_smem(p))) != cudaSuccess) return e;
+  gdn_simt_chain<T, false><<<dim3((p.DV + kVT - 1) / kVT, p.BH), kThreads, chain_smem(p), st>>>(
+      p, (const T*)x.K, x.beta, x.C0, C_T, nullptr, w);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t fw(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T, void* ws,
                cudaStream_t st) {
   const Ws w = layout(p, false, static_cast<char*>(ws));
-  if (p.T > 0) {
-    const cudaError_t e = prep<T>(p, x, w, st);
-    if (e != cudaSuccess) return e;
-  }
-  const cudaError_t e = allow(gdn_simt_chain<T, true>, chain_smem(p));
+  cudaError_t e = states<T, false>(p, x, nullptr, C_T, w, st);
   if (e != cudaSuccess) return e;
-  gdn_simt_chain<T, true><<<dim3((p.DV + kVT - 1) / kVT, p.BH), kThreads, chain_smem(p), st>>>(
-      p, (const T*)x.Q, (const T*)x.K, (const T*)x.V, x.beta, x.C0, (T*)H, C_T, w);
+  if ((e = allow(gdn_simt_out<T>, kOutSmem)) != cudaSuccess) return e;
+  gdn_simt_out<T><<<dim3((p.DV + 63) / 64, chunks_of(p.T), p.BH), kThreads, kOutSmem, st>>>(
+      p, (const T*)x.Q, x.beta, (T*)H, w);
   return cudaGetLastError();
 }
 
@@ -694,16 +716,12 @@ template <typename T>
 cudaError_t bw(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, void* ws,
                cudaStream_t st) {
   const Ws w = layout(p, true, static_cast<char*>(ws));
-  const dim3 cols((p.DV + kVT - 1) / kVT, p.BH), chunks(chunks_of(p.T), p.BH);
-  cudaError_t e = prep<T>(p, x, w, st);
+  const dim3 chunks(chunks_of(p.T), p.BH);
+  cudaError_t e = states<T, true>(p, x, d.dH, nullptr, w, st);
   if (e != cudaSuccess) return e;
-  if ((e = allow(gdn_simt_chain<T, false>, chain_smem(p))) != cudaSuccess) return e;
-  gdn_simt_chain<T, false><<<cols, kThreads, chain_smem(p), st>>>(
-      p, (const T*)x.Q, (const T*)x.K, (const T*)x.V, x.beta, x.C0, nullptr, nullptr, w);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = allow(gdn_simt_bchain<T>, chain_smem(p))) != cudaSuccess) return e;
-  gdn_simt_bchain<T><<<cols, kThreads, chain_smem(p), st>>>(
-      p, (const T*)x.Q, (const T*)x.K, x.beta, (const T*)d.dH, d.dC_T, (T*)d.dV, d.dC0, w);
+  if ((e = allow(gdn_simt_chain<T, true>, chain_smem(p))) != cudaSuccess) return e;
+  gdn_simt_chain<T, true><<<dim3((p.DV + kVT - 1) / kVT, p.BH), kThreads, chain_smem(p), st>>>(
+      p, (const T*)x.K, x.beta, d.dC_T, d.dC0, (T*)d.dV, w);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = allow(gdn_simt_grads<T>, kGradSmem)) != cudaSuccess) return e;
   gdn_simt_grads<T><<<chunks, kThreads, kGradSmem, st>>>(p, (const T*)x.Q, (const T*)x.K, x.beta,
@@ -720,7 +738,7 @@ size_t gdn_simt_workspace(const GdnProblem& p, bool backward) {
   return layout(p, backward, nullptr).bytes;
 }
 int gdn_simt_launches(const GdnProblem& p, bool backward) {
-  return backward ? 4 + (p.group > 1) : 1 + (p.T > 0);
+  return backward ? 5 + (p.group > 1) : 4;
 }
 cudaError_t launch_gdn_simt_fw(const GdnProblem& p, mlstm_dtype dt, const GdnInputs& x, void* H,
                                float* C_T, void* ws, cudaStream_t st) {
