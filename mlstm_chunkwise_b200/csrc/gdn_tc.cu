@@ -272,7 +272,7 @@ constexpr size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Parts of the workspace.  kKeep: what outlives the forward of the training pair
 // beside kState; kInverse and kN of the forward do not.
-enum : int { kState = 1, kKeep = 2, kInverse = 4, kN = 8, kGrad = 16 };
+enum : int { kSums = 1, kState = 2, kKeep = 4, kInverse = 8, kN = 16, kGrad = 32 };
 
 // Sets the pointers of `parts` in w from `base` on; returns their bytes.
 size_t carve(const GdnProblem& p, int parts, const void* base, GdnTcWs* w) {
@@ -287,8 +287,8 @@ size_t carve(const GdnProblem& p, int parts, const void* base, GdnTcWs* w) {
     at += round256(bytes);
     return r;
   };
+  if (parts & kSums) w->gc = reinterpret_cast<float2*>(take(nc * kGdnL * sizeof(float2)));
   if (parts & kState) {
-    w->gc = reinterpret_cast<float2*>(take(nc * kGdnL * sizeof(float2)));
     w->M = take(nc * 4 * tc::kBlk);
     w->S = take(tile);
   }
@@ -310,8 +310,11 @@ size_t carve(const GdnProblem& p, int parts, const void* base, GdnTcWs* w) {
   }
   return at;
 }
-constexpr int kFwParts = kState | kInverse | kN;
-constexpr int kBwParts = kState | kKeep | kInverse | kN | kGrad;
+int fw_parts(const GdnProblem& p) {
+  return kSums | kInverse | (gdn_tc_fw_fused(p) ? 0 : kState | kN);
+}
+constexpr int kBwParts = kSums | kState | kKeep | kInverse | kN | kGrad;
+constexpr int kSaved = kSums | kState | kKeep;
 
 bool map16(CUtensorMap* m, const void* base, int cols, int T, long heads) {
   return encode_tmap_bf16_3d(m, base, cols, T, heads, 64, kGdnL);
@@ -326,6 +329,7 @@ cudaError_t forward(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T
   if (!H) m.h = m.v;
   cudaError_t e = launch_gdn_tc_inverse(p, x, m, w, st);
   if (e != cudaSuccess) return e;
+  if (!w.M) return launch_gdn_tc_scan(p, x, m, C_T, w, st);
   if ((e = launch_gdn_tc_mn(p, x, m, w, st)) != cudaSuccess) return e;
   if ((e = launch_gdn_tc_chain(p, false, x.C0, C_T, w, st)) != cudaSuccess) return e;
   return launch_gdn_tc_out(p, x, m, H != nullptr, w, st);
@@ -376,11 +380,11 @@ cudaError_t gdn_allow_smem(const void* kern, size_t smem) {
 
 size_t gdn_tc_workspace(const GdnProblem& p, bool backward) {
   GdnTcWs w{};
-  return p.T > 0 ? carve(p, backward ? kBwParts : kFwParts, nullptr, &w) : 0;
+  return p.T > 0 ? carve(p, backward ? kBwParts : fw_parts(p), nullptr, &w) : 0;
 }
 GdnTrainSizes gdn_tc_train_sizes(const GdnProblem& p) {
   GdnTcWs w{};
-  return {carve(p, kState | kKeep, nullptr, &w), carve(p, kInverse | kN, nullptr, &w),
+  return {carve(p, kSaved, nullptr, &w), carve(p, kInverse | kN, nullptr, &w),
           carve(p, kN | kGrad, nullptr, &w)};
 }
 
@@ -388,7 +392,7 @@ int gdn_tc_train_launches(const GdnProblem& p, bool backward) {
   return backward ? 4 + (p.group > 1) : 4;
 }
 int gdn_tc_launches(const GdnProblem& p, bool backward) {
-  return backward ? 4 + gdn_tc_train_launches(p, true) : 4;
+  return backward ? 4 + gdn_tc_train_launches(p, true) : gdn_tc_fw_fused(p) ? 2 : 4;
 }
 
 cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
@@ -404,7 +408,7 @@ cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, const Gdn
 cudaError_t launch_gdn_tc_fw(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T,
                              void* ws, cudaStream_t st) {
   GdnTcWs w{};
-  carve(p, kFwParts, ws, &w);
+  carve(p, fw_parts(p), ws, &w);
   GdnMaps m;
   return forward(p, x, H, C_T, m, w, st);
 }
@@ -419,7 +423,7 @@ cudaError_t launch_gdn_tc_bw(const GdnProblem& p, const GdnInputs& x, const GdnG
 cudaError_t launch_gdn_tc_fw_train(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T,
                                    void* saved, void* ws, cudaStream_t st) {
   GdnTcWs w{};
-  carve(p, kState | kKeep, saved, &w);
+  carve(p, kSaved, saved, &w);
   carve(p, kInverse | kN, ws, &w);
   GdnMaps m;
   return forward(p, x, H, C_T, m, w, st);
@@ -427,7 +431,7 @@ cudaError_t launch_gdn_tc_fw_train(const GdnProblem& p, const GdnInputs& x, void
 cudaError_t launch_gdn_tc_bw_saved(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d,
                                    const void* saved, void* ws, cudaStream_t st) {
   GdnTcWs w{};
-  carve(p, kState | kKeep, saved, &w);
+  carve(p, kSaved, saved, &w);
   carve(p, kN | kGrad, ws, &w);
   GdnMaps m;
   return backward(p, x, d, false, m, w, st);

@@ -135,6 +135,10 @@ cudaError_t launch_gdn_tc_chain(const GdnProblem& p, bool reverse, const float* 
 // with_h: H, else y alone.
 cudaError_t launch_gdn_tc_out(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
                               bool with_h, const GdnTcWs& w, cudaStream_t st);
+// The forward fused, behind the inverse: instead of mn, chain and out.
+bool gdn_tc_fw_fused(const GdnProblem& p);
+cudaError_t launch_gdn_tc_scan(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m, float* C_T,
+                               const GdnTcWs& w, cudaStream_t st);
 // after: behind another stage (else first in its call).
 cudaError_t launch_gdn_tc_dz0(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m, bool after,
                               const GdnTcWs& w, cudaStream_t st);

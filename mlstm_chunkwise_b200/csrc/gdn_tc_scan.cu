@@ -1,0 +1,316 @@
+// Gated delta rule on the tensor cores: the forward of many heads, fused.
+//
+// A block walks the chunks of one (bh, up to 128 value columns) with the state in
+// tensor memory, so that M, N and the chunks' states never reach memory: 210 KB
+// of traffic per 128 tokens against 730 KB of the staged forward.  Per chunk:
+//   1  X = K S, Q S           meanwhile Tinv to tensor memory
+//      z = V - Lam X
+//   2  y = Tinv z             meanwhile Q S is scaled in place
+//      the images of y and of D beta y
+//   3  S = e^G S + K^T (D beta y), Q K^T
+//      P
+//   4  H = scale (Lam Q S + P y)   meanwhile the next state's image, e^G S
+// Four dependent rounds, 104 products of 128 x 128 x 16 (7300 cycles) and about as
+// long in passes: slower per chunk than the staged forward where few heads leave
+// SMs idle, see gdn_tc_fw_fused().
+// Tensor memory: S [0, 128), X and y [128, 256), Tinv then Q K^T and P [256, 384),
+// Q S then H [384, 512).  Shared memory blocks: K 0, 1; Q 2, 3; V 4, 5; z, y, H 6..9;
+// D beta y, then the state's image 10..13.
+#include <cuda.h>
+
+#include "gdn_tc.h"
+
+namespace mlstm {
+namespace {
+
+using namespace tc;
+
+constexpr uint32_t kOffQ = 2 * kBlk, kOffV = 4 * kBlk, kOffZ = 6 * kBlk, kOffU = 10 * kBlk;
+constexpr uint32_t kOffGc = 14 * kBlk;            // float2[128]
+constexpr uint32_t kOffBeta = kOffGc + 1024;      // float[128]
+constexpr uint32_t kOffCol = kOffBeta + 512;      // float[2][128], as in gdn_tc.cu
+constexpr uint32_t kOffBar = kOffCol + 1024;
+constexpr uint32_t kSmem = kOffBar + 64;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+__global__ void __launch_bounds__(kGdnThreads, 1)
+gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_h, GdnProblem p,
+                   const float* __restrict__ beta, const float* __restrict__ C0,
+                   float* __restrict__ C_T, GdnTcWs w) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  float2* gc = reinterpret_cast<float2*>(smem + kOffGc);
+  float* sbeta = reinterpret_cast<float*>(smem + kOffBeta);
+  float* scol = reinterpret_cast<float*>(smem + kOffCol);
+  const uint32_t ka = sbase, qa = sbase + kOffQ, va = sbase + kOffV, za = sbase + kOffZ,
+                 ua = sbase + kOffU;
+  const uint32_t bar_qk = sbase + kOffBar, bar_v = bar_qk + 8;
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
+  const bool row = tid < kGdnRows, lead = tid == kGdnRows;
+  const int slabs = (p.DK + 63) / 64;
+  const int vt = blockIdx.x * 2, bh = blockIdx.y, NC = w.NC, tiles = min(2, w.nvt - vt);
+  const bool cols = row && h < 2 * tiles;
+  const int v0 = vt * 64 + h * 32;  // first value column of this thread
+  const int kh = gdn_key_head(p, bh);
+  GdnRounds rd{bar_qk + 16, 0u, true, Problem{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls}};
+  auto load_qk = [&](int c) {
+    mbar_expect_tx(bar_qk, 2 * slabs * kBlk);
+    for (int s = 0; s < slabs; ++s) {
+      tma_load_3d(ka + s * kBlk, &tm_k, s * 64, c * kGdnL, kh, bar_qk);
+      tma_load_3d(qa + s * kBlk, &tm_q, s * 64, c * kGdnL, kh, bar_qk);
+    }
+  };
+  auto load_v = [&](int c) {
+    mbar_expect_tx(bar_v, tiles * kBlk);
+    for (int v = 0; v < tiles; ++v)
+      tma_load_3d(va + v * kBlk, &tm_v, (vt + v) * 64, c * kGdnL, bh, bar_v);
+  };
+  uint4 ti[8];
+  float2 ng, ngl;
+  float nb;
+  auto load_gates = [&](int c) {
+    const size_t at = ((size_t)bh * NC + c) * kGdnL;
+    ng = w.gc[at + r];
+    ngl = w.gc[at + kGdnL - 1];
+    nb = c * kGdnL + r < p.T ? beta[(long)bh * p.T + c * kGdnL + r] : 0.f;
+  };
+
+  if (lead) {
+    for (int i = 0; i < 3; ++i) mbar_init(bar_qk + 8 * i, 1);
+    fence_barrier_init();
+    load_qk(0);
+    load_v(0);
+  }
+  if (!row) {
+    __syncwarp();
+    tmem_alloc(smem_u32((const void*)slot), 512);
+    tmem_relinquish();
+  }
+  gdn_wait_stage();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16), trow = tlane + h * 32;
+  uint8_t *img = smem + kOffZ + (h >> 1) * kBlk, *imgu = smem + kOffU + (h >> 1) * kBlk;
+  const uint32_t id = idesc_bf16(128, tiles * 64, 0, 1), idt = idesc_bf16(128, tiles * 64, 1, 1);
+
+  // the state's row r (of d_qk), columns 32 h ..: its image, and e^G times it
+  auto split_state = [&](uint32_t (&v)[32], float eg) {
+#pragma unroll
+    for (int cc = 0; cc < 4; ++cc)
+      put8(imgu, 2 * kBlk, r, (h & 1) * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(eg * __uint_as_float(v[e]));
+    tmem_st32(trow, v);
+  };
+  if (row) load_gates(0);
+  if (cols) {
+    uint32_t v[32];
+    const float* src = C0 + ((long)bh * p.DK + r) * p.DV + v0;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const bool in = C0 && r < p.DK && v0 + e < p.DV;
+      const float4 x = in ? *reinterpret_cast<const float4*>(src + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[e] = __float_as_uint(x.x);
+      v[e + 1] = __float_as_uint(x.y);
+      v[e + 2] = __float_as_uint(x.z);
+      v[e + 3] = __float_as_uint(x.w);
+    }
+    split_state(v, gdn_exp(ngl));
+  }
+
+  for (int c = 0; c < NC; ++c) {
+    const uint32_t ph = c & 1;
+    const bool more = c + 1 < NC;
+    float2 gr = make_float2(0.f, 0.f);
+    float dec = 0.f;
+    if (row) {
+      gr = ng;
+      dec = nb * gdn_decay(ngl, gr);
+      if (h == 0) {
+        gc[r] = gr;
+        sbeta[r] = nb;
+        scol[r] = nb * gdn_col_factor(gr, 31);
+        scol[128 + r] = __fdividef(nb, gdn_col_factor(gr, 0));
+      }
+      load_tinv(w.tinv + ((size_t)bh * NC + c) * 32 * 128, r, h, h <= q, ti);
+    }
+    const float lam = gdn_exp(gr);
+    uint32_t v[32];
+    gdn_round(
+        rd, 0x81,
+        [&] {
+          rd.ok = mbar_wait(bar_qk, ph, rd.wt, 0x80);
+          tc_fence_after();
+          if (!rd.ok) return;
+          for (int t = 0; t < 2; ++t)
+            mma_ss<false, true>(tmem + 128, ka, ua + 2 * t * kBlk, id, slabs, t == 0);
+          for (int t = 0; t < 2; ++t)
+            mma_ss<false, true>(tmem + 384, qa, ua + 2 * t * kBlk, id, slabs, t == 0);
+        },
+        [&] {
+          add_identity(r, h, ti);
+          put_tinv(tlane + 256, h, ti);
+          if (more) load_gates(c + 1);
+          if (rd.ok) rd.ok = mbar_wait(bar_v, ph, rd.wt, 0x85);
+        },
+        gdn_nothing, gdn_nothing);
+    if (cols) {
+      tmem_ld32(trow + 128, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        float z[8];
+        unpack8(*reinterpret_cast<const uint4*>(smem + kOffV + (h >> 1) * kBlk +
+                                                sw128_offset(r, (h & 1) * 4 + cc)),
+                z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = fmaf(-lam, __uint_as_float(v[8 * cc + e]), z[e]);
+        put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, z);
+      }
+    }
+    gdn_round(
+        rd, 0x82, [&] { mma_terms3(tmem + 128, tmem + 256, za, 2 * kBlk, id); },
+        [&] {
+          if (!cols) return;
+          const float f = p.scale * lam;
+          tmem_ld32(trow + 384, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
+          tmem_st32(trow + 384, v);
+        },
+        [&] {
+          if (more) load_v(c + 1);
+        },
+        gdn_nothing);
+    if (cols) {
+      tmem_ld32(trow + 128, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[8 * cc + e]);
+        put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= dec;
+        put8(imgu, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+      }
+    }
+    gdn_round(
+        rd, 0x83,
+        [&] {
+          mma_ss<false, false>(tmem + 256, qa, ka, idesc_bf16(128, 128, 0, 0), slabs, true);
+          for (int t = 0; t < 2; ++t)
+            mma_ss<true, true>(tmem, ka, ua + 2 * t * kBlk, idt, 2, false);
+        },
+        gdn_nothing, gdn_nothing,
+        [&] {
+          if (more) load_qk(c + 1);
+        });
+    if (row) {  // P: 32 keys of the row; its terms take the scores' columns, hi then lo
+      uint32_t hi[16], lo[16];
+      if (h <= q) {
+        tmem_ld32(trow + 256, v);
+        tmem_wait_ld();
+        float s[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = p.scale * __uint_as_float(v[e]);
+        if (h == q && gc[h * 32].x - gc[h * 32 + 31].x > kGdnFlat) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int k = h * 32 + e;
+            s[e] = e <= lane ? gdn_decay(gr, gc[k]) * sbeta[k] * s[e] : 0.f;
+          }
+        } else {
+          const bool d = h == q;
+          const float f = gdn_decay(gr, gc[h * 32 + (d ? 0 : 31)]);
+          const float* sc = scol + (d ? 128 : 0) + h * 32;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e] = d && e > lane ? 0.f : s[e] * (f * sc[e]);
+        }
+        split_pack<32>(s, hi, lo);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
+      }
+      tmem_st16(trow + 256, hi);
+      tmem_st16(trow + 272, lo);
+    }
+    gdn_round(
+        rd, 0x84,
+        [&] {
+#pragma unroll
+          for (int t = 0; t < 3; ++t)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(tmem + 384,
+                          tmem + 256 + (kk >> 1) * 32 + (t == 1 ? 16 : 0) + (kk & 1) * 8,
+                          mnmaj(za + (t == 2 ? 2 * kBlk : 0u), kk), id, 1);
+        },
+        [&] {
+          if (!cols) return;
+          tmem_ld32(trow, v);
+          tmem_wait_ld();
+          if (more) {
+            split_state(v, gdn_exp(ngl));
+          } else if (C_T && r < p.DK && rd.ok) {
+            float* dst = C_T + ((long)bh * p.DK + r) * p.DV + v0;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (v0 + e < p.DV)
+                *reinterpret_cast<float4*>(dst + e) =
+                    make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                                __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+          }
+        },
+        gdn_nothing, gdn_nothing);
+    if (cols) {
+      tmem_ld32(trow + 384, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc)
+        *reinterpret_cast<uint4*>(img + sw128_offset(r, (h & 1) * 4 + cc)) =
+            pack8(reinterpret_cast<const float*>(v) + 8 * cc);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (lead && rd.ok) {  // rows past T and columns past d_v are clipped
+      for (int t = 0; t < tiles; ++t)
+        tma_store_3d(&tm_h, za + t * kBlk, (vt + t) * 64, c * kGdnL, bh);
+      tma_store_commit();
+      tma_store_wait_read_all();  // before z takes its place, behind the next round
+    }
+  }
+  if (lead) tma_store_wait_all();
+  __syncthreads();
+  if (!row) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+// A chunk costs a fused block about 7 us, the staged forward 19 us of one SM (mn
+// and out) and its recurrence 1.4 us: the fused one wins from about 48 (bh, pair
+// of value tiles) on, a third of the SMs.
+bool gdn_tc_fw_fused(const GdnProblem& p) {
+  return (long)p.BH * ((p.DV + 127) / 128) >= 48;
+}
+
+cudaError_t launch_gdn_tc_scan(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m, float* C_T,
+                               const GdnTcWs& w, cudaStream_t st) {
+  return gdn_launch(&gdn_tc_scan_kernel, dim3((w.nvt + 1) / 2, p.BH), kGdnThreads, kSmem, true, st,
+                    m.q, m.k, m.v, m.h, p, x.beta, x.C0, C_T, w);
+}
+
+}  // namespace mlstm

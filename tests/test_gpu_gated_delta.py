@@ -88,6 +88,25 @@ def test_sizes(algo, dtype, size):
     run_case(algo, dict(B=B, NHK=NHK, NH=NH, T=T, DK=DK, DV=DV, dtype=dtype))
 
 
+# enough heads (times pairs of 64 value columns) for the fused forward
+MANY_HEADS = [(12, 2, 4, 77, 64, 72), (6, 4, 8, 300, 128, 128), (24, 1, 2, 129, 96, 64),
+              (7, 1, 4, 260, 8, 200), (16, 1, 3, 1, 128, 128), (1, 16, 64, 385, 128, 64)]
+
+
+@pytest.mark.parametrize("size", MANY_HEADS, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("init", [True, False])
+def test_many_heads(size, init):
+    B, NHK, NH, T, DK, DV = size
+    run_case("tc", dict(B=B, NHK=NHK, NH=NH, T=T, DK=DK, DV=DV, init=init), backward=T < 100)
+
+
+@pytest.mark.parametrize("gates", ["strong", "hold", "zero_beta", "reset"])
+@pytest.mark.parametrize("keys", ["unit", "alike"])
+def test_many_heads_gates_and_keys(gates, keys):
+    run_case("tc", dict(B=12, NHK=2, NH=4, T=333, DK=128, DV=128, gates=gates, keys=keys, seed=3),
+             backward=False)
+
+
 @pytest.mark.parametrize("algo", ALGOS)
 @pytest.mark.parametrize("gates", ["strong", "hold", "zero_beta", "reset"])
 @pytest.mark.parametrize("keys", ["unit", "alike"])
