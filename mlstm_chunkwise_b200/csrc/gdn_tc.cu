@@ -132,6 +132,9 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
         },
         [&] {
+          add_identity(r, h, ti);
+          put_tinv(tlane, h, ti);
+          if (more) load_gates(nx);
           if (rd.ok) rd.ok = mbar_wait(bar_v, in_phase, rd.wt, 0x65);
         },
         gdn_nothing,
@@ -140,11 +143,6 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         });
     const float lam = gdn_exp(gr);
     uint32_t v[32];
-    if (row) {
-      add_identity(r, h, ti);
-      put_tinv(tlane, h, ti);
-      if (more) load_gates(nx);
-    }
     if (cols) {
       tmem_ld32(trow + 256, v);
       tmem_wait_ld();

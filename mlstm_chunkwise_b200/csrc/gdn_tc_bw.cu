@@ -178,7 +178,11 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int t = 0; t < 2; ++t)
             mma_ss<true, true>(tmem + 384, qa, la + 2 * t * kBlk, idt, 2, t == 0);
         },
-        gdn_nothing, gdn_nothing, gdn_nothing);
+        [&] {
+          add_identity(r, h, ti);
+          put_tinv(tlane + 128, h, ti);
+        },
+        gdn_nothing, gdn_nothing);
     auto put = [&](float f) {  // f times the 32 columns in v
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
@@ -188,10 +192,6 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         put8(smem + kZW + at, 2 * kBlk, r, (h & 1) * 4 + cc, y);
       }
     };
-    if (row) {
-      add_identity(r, h, ti);
-      put_tinv(tlane + 128, h, ti);
-    }
     if (cols) {
       tmem_ld32(trow + 256, v);
       tmem_wait_ld();
@@ -346,6 +346,8 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
             mma_ss<false, true>(tmem + 128, ka, da + 2 * t * kBlk, id, slabs, t == 0);
         },
         [&] {
+          add_identity(r, h, ti);
+          put_tinv(tlane, h, ti);
           if (rd.ok) rd.ok = mbar_wait(bar_y, in_phase, rd.wt, 0x75);
         },
         gdn_nothing,
@@ -353,10 +355,6 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
           if (more) load_tiles(nx, false);
         });
     uint32_t v[32];
-    if (row) {
-      add_identity(r, h, ti);
-      put_tinv(tlane, h, ti);
-    }
     if (cols) {
       tmem_ld32(trow + 128, v);
       tmem_wait_ld();

@@ -345,7 +345,6 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   gdn_wait_stage();
   if (row) {
     load_rows(x);
-    if (h == 0) slam[r] = gdn_exp(ngc);
   }
   tc_fence_before();
   __syncthreads();
@@ -353,6 +352,34 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const uint32_t tmem = *slot;
   const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16), trow = tlane + h * 32;
   uint32_t in_phase = 0;
+  // Tinv and Tinv Lam of the item that load_rows() fetched: under the second round
+  // of the item before, which needs neither of its own
+  auto put_operands = [&](bool with_lam) {
+    if (h == 0) slam[r] = gdn_exp(ngc);
+    add_identity(r, h, ti);
+    put_tinv(tlane, h, ti);
+    if (!with_lam) return;
+    named_bar_sync(1, kGdnRows);
+    uint32_t hi[16], lo[16];
+    if (h <= q) {
+      float y[32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float a[8], b[8];
+        unpack8(ti[k], a);
+        unpack8(ti[4 + k], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[8 * k + e] = (a[e] + b[e]) * slam[h * 32 + 8 * k + e];
+      }
+      split_pack<32>(y, hi, lo);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
+    }
+    tmem_st16(tlane + 384 + h * 16, hi);
+    tmem_st16(tlane + 448 + h * 16, lo);
+  };
+  if (row) put_operands(true);
 
   for (long i = blockIdx.x; i < items; i += gridDim.x, in_phase ^= 1) {
     const bool more = i + gridDim.x < items;
@@ -361,32 +388,7 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t nk = idesc_bf16(128, slabs * 64, 0, 1), nkt = idesc_bf16(128, slabs * 64, 1, 1);
     const uint32_t nv = idesc_bf16(128, x.tiles * 64, 0, 1),
                    nvt = idesc_bf16(128, x.tiles * 64, 1, 1);
-    float dec = 0.f;
-    if (row) {
-      dec = nbt * gdn_decay(ngl, ngc);
-      add_identity(r, h, ti);
-      put_tinv(tlane, h, ti);
-      if (first) {  // Tinv Lam
-        uint32_t hi[16], lo[16];
-        if (h <= q) {
-          float y[32];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float a[8], b[8];
-            unpack8(ti[k], a);
-            unpack8(ti[4 + k], b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[8 * k + e] = (a[e] + b[e]) * slam[h * 32 + 8 * k + e];
-          }
-          split_pack<32>(y, hi, lo);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
-        }
-        tmem_st16(tlane + 384 + h * 16, hi);
-        tmem_st16(tlane + 448 + h * 16, lo);
-      }
-    }
+    const float dec = row ? nbt * gdn_decay(ngl, ngc) : 0.f;
     if (lead) tma_store_wait_read_all();  // M of the item before has left
     gdn_round(
         rd, 0x47,
@@ -398,7 +400,10 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           if (first) mma_terms2(tmem + 128, tmem + 384, ka, nk);
           mma_terms2(tmem + 256, tmem, va, nv);
         },
-        gdn_nothing, gdn_nothing,
+        [&] {
+          if (more) load_rows(nx);
+        },
+        gdn_nothing,
         [&] {
           if (more) load_v(nx);
         });
@@ -437,7 +442,7 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mma_ss<true, true>(tmem + 256, ka, ua + 2 * t * kBlk, nvt, 2, t == 0);
         },
         [&] {
-          if (more) load_rows(nx);
+          if (more) put_operands(nx.vt == 0);
         },
         gdn_nothing,
         [&] {
@@ -461,7 +466,6 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           dst[e * 128] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                                      __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
       }
-      if (more && h == 0) slam[r] = gdn_exp(ngc);
     }
     fence_proxy_async_smem();
     tc_fence_before();
