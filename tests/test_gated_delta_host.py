@@ -92,6 +92,62 @@ def test_bw_pointers(L, name):
     assert bw(**{name: O if name in GATES else U}) == _lib.ERR_INVALID_ARG
 
 
+def train_sizes(B=1, NHK=2, NH=4, T=100, DK=64, DV=64, dt=_lib.DT_BF16):
+    z = [ctypes.c_size_t(0) for _ in range(3)]
+    st = _lib.lib().mlstm_gated_delta_train_sizes(B, NHK, NH, T, DK, DV, dt,
+                                                  *(ctypes.byref(n) for n in z))
+    return st, [n.value for n in z]
+
+
+def test_train_sizes(L):
+    st, (saved, fw_ws, bw_ws) = train_sizes()
+    assert st == _lib.OK and min(saved, fw_ws, bw_ws) > 0
+    # the three together hold what the recomputing backward needs
+    assert saved + fw_ws + bw_ws >= size(algo=_lib.ALGO_TC, bw=1)[1]
+    for kw in (dict(dt=_lib.DT_F32), dict(DK=136), dict(DK=60), dict(DV=12), dict(T=0),
+               dict(T=15)):  # 4 x 15 tokens: AUTO's gradients take the fp32 path
+        assert train_sizes(**kw)[0] == _lib.ERR_UNSUPPORTED, kw
+    for kw in (dict(B=0), dict(NHK=3), dict(T=-1), dict(dt=7)):
+        assert train_sizes(**kw)[0] == _lib.ERR_INVALID_ARG, kw
+    n = ctypes.c_size_t(0)
+    assert L.mlstm_gated_delta_train_sizes(1, 1, 1, 100, 64, 64, _lib.DT_BF16, None,
+                                           ctypes.byref(n), ctypes.byref(n)) == \
+        _lib.ERR_INVALID_ARG
+    assert api.gated_delta_train_sizes(1, 2, 4, 100, 64, 64) == (saved, fw_ws, bw_ws)
+    assert api.gated_delta_train_sizes(1, 2, 4, 100, 64, 64, torch.float32) is None
+
+
+def fw_train(**over):
+    a = dict(Q=P, K=P, V=P, g=P, beta=P, C0=None, H=P, C_T=None, saved=P, sb=1 << 40, B=1, NHK=1,
+             NH=2, T=64, DK=64, DV=64, scale=1.0, dt=_lib.DT_BF16, ws=P, wsb=1 << 40)
+    a.update(over)
+    return _lib.lib().mlstm_gated_delta_fw_train(*a.values(), None)
+
+
+def bw_saved(**over):
+    a = dict(Q=P, K=P, V=P, g=P, beta=P, saved=P, sb=1 << 40, dH=P, dC_T=None, dQ=P, dK=P, dV=P,
+             dg=P, dbeta=P, dC0=None, B=1, NHK=1, NH=2, T=64, DK=64, DV=64, scale=1.0,
+             dt=_lib.DT_BF16, ws=P, wsb=1 << 40)
+    a.update(over)
+    return _lib.lib().mlstm_gated_delta_bw_saved(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [fw_train, bw_saved])
+def test_training_pair_refusals(L, call):
+    names = ["Q", "K", "V", "g", "beta", "saved", "ws"] + \
+        (["H"] if call is fw_train else ["dH", "dQ", "dK", "dV", "dg", "dbeta"])
+    for n in names:
+        assert call(**{n: None}) == _lib.ERR_INVALID_ARG, n
+        assert call(**{n: O if n in GATES else U}) == _lib.ERR_INVALID_ARG, n
+    assert call(sb=64) == _lib.ERR_INVALID_ARG
+    assert call(wsb=64) == _lib.ERR_INVALID_ARG
+    assert call(scale=float("inf")) == _lib.ERR_INVALID_ARG
+    assert call(NHK=3) == _lib.ERR_INVALID_ARG
+    assert call(dt=_lib.DT_F32) == _lib.ERR_UNSUPPORTED
+    assert call(DK=256) == _lib.ERR_UNSUPPORTED
+    assert call(T=0) == _lib.ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta", "C", "h"])
 def test_step_pointers(L, name):
     assert step(**{name: None}) == _lib.ERR_INVALID_ARG
@@ -142,6 +198,12 @@ def test_binding_refuses(L):
         api.gated_delta_fw(q, q, q, g, g)
     with pytest.raises(ValueError, match="CUDA tensor"):
         api.gated_delta_bw(q, q, q, g, g, q)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        api.gated_delta_fw_train(q, q, q, g, g)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        api.gated_delta_bw_saved(q, q, q, g, g, torch.zeros(8, dtype=torch.uint8), q)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        api.gated_delta_chunkwise(q, q, q, g, g)
     with pytest.raises(ValueError, match="CUDA tensor"):
         api.gated_delta_step(q[:, :, 0], q[:, :, 0], q[:, :, 0], g[:, :, 0], g[:, :, 0],
                              torch.zeros(1, 2, 8, 8))

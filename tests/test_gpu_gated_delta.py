@@ -75,6 +75,9 @@ SIZES = [
     (1, 2, 2, 70, 33, 7),
     (1, 1, 1, 100, 256, 512),    # the 7B head
     (1, 1, 1, 66, 1024, 40),     # the widest key
+    (1, 1, 2, 200, 64, 512),     # several pairs of value tiles
+    (1, 1, 1, 130, 128, 1000),
+    (1, 2, 2, 40, 16, 8),
 ]
 
 
@@ -268,6 +271,48 @@ def test_repeat_calls_agree_bit_for_bit():
         now = [H, C, *g.values()]
         first = first or now
         assert all(torch.equal(a, b) for a, b in zip(first, now))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_inputs_are_checked(dtype):
+    """What the binding refuses with tensors on the GPU: shapes, types, strides."""
+    x = gd.cuda(gd.make(NHK=1, NH=2, T=64, DK=64, DV=64, dtype=dtype))
+    a = [x[n] for n in gd.NAMES]
+
+    def refuse(match, i, bad, call=api.gated_delta_fw):
+        with pytest.raises(ValueError, match=match):
+            call(*(bad if j == i else t for j, t in enumerate(a)))
+
+    refuse("contiguous", 0, x["Q"].transpose(2, 3).contiguous().transpose(2, 3))
+    refuse("shape", 1, x["K"][:, :, :-1].contiguous())
+    refuse("shape", 3, x["g"][:, :1].contiguous())
+    refuse("float32", 4, x["beta"].double())
+    refuse("shape", 5, x["C0"][..., :-1].contiguous())
+    refuse("CUDA tensor", 2, x["V"].cpu())
+    out = torch.empty_like(x["V"])[:, :, :-1]
+    with pytest.raises(ValueError, match="shape"):
+        api.gated_delta_fw(*a, out={"H": out})
+    with pytest.raises(ValueError, match="workspace"):
+        api.gated_delta_fw(*a, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    if dtype == "bf16":
+        _, _, saved = api.gated_delta_fw_train(*a)
+        with pytest.raises(ValueError, match="shape"):
+            api.gated_delta_bw_saved(*a[:5], saved[:-16].contiguous(), x["V"], a[5])
+    torch.cuda.synchronize()
+    assert api.last_device_error() == _lib.OK
+
+
+def test_a_workspace_of_the_callers_holds_other_data():
+    """Nothing is read from the workspace before it is written."""
+    for kw in (dict(T=200), dict(B=12, NHK=4, NH=4, T=200), dict(T=200, dtype="f32")):
+        x = gd.cuda(gd.make(DK=64, DV=64, **kw))
+        a = [x[n] for n in gd.NAMES]
+        want = api.gated_delta_fw(*a)
+        B, NHK, T, DK = x["Q"].shape
+        n = api.gated_delta_workspace_size(B, NHK, x["V"].shape[1], T, DK, 64, x["Q"].dtype)
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN in every type
+        got = api.gated_delta_fw(*a, workspace=ws)
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
 
 
 def test_two_streams_at_once():
