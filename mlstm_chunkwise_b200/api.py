@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -424,8 +425,11 @@ def _check_gated_delta(Q, K, V, g, beta, C0, T_dims):
     return B, NHK, NH, DK, DV, dev, dt
 
 
+@functools.lru_cache(maxsize=1024)  # sizes alone decide it
 def gated_delta_workspace_size(B, NHK, NH, T, DK, DV, dtype=torch.bfloat16, algo="auto",
                                backward=False) -> int:
+    """Bytes of workspace of ``gated_delta_fw`` (or, ``backward``, of
+    ``gated_delta_bw``)."""
     n = ctypes.c_size_t(0)
     _lib.check(_lib.lib().mlstm_gated_delta_workspace_size(
         B, NHK, NH, T, DK, DV, _DT[dtype], _ALGO[algo], int(backward), ctypes.byref(n)),
@@ -458,11 +462,13 @@ def gated_delta_fw(Q, K, V, g, beta, C0=None, *, scale: float | None = None, alg
     out = {} if out is None else out
     H, C_T = out.get("H"), out.get("C_T") if return_last_state else None
     if H is None:
-        H = torch.empty((B, NH, T, DV), dtype=dt, device=dev)
+        H = torch.empty_like(V)
+    else:
+        _check_tensor("H", H, dt, (B, NH, T, DV), dev)
     if C_T is None and return_last_state:
-        C_T = torch.empty((B, NH, DK, DV), dtype=torch.float32, device=dev)
-    _check_tensor("H", H, dt, (B, NH, T, DV), dev)
-    _check_tensor("C_T", C_T, torch.float32, (B, NH, DK, DV), dev)
+        C_T = g.new_empty((B, NH, DK, DV))
+    else:
+        _check_tensor("C_T", C_T, torch.float32, (B, NH, DK, DV), dev)
     ws_bytes = gated_delta_workspace_size(B, NHK, NH, T, DK, DV, dt, algo)
     if workspace is None:
         workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
@@ -514,6 +520,7 @@ def gated_delta_bw(Q, K, V, g, beta, dH, C0=None, dC_T=None, *, scale: float | N
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def gated_delta_train_sizes(B, NHK, NH, T, DK, DV, dtype=torch.bfloat16):
     """Bytes of the saved buffer and of the two calls' workspaces of the
     training pair, or None where it does not exist (it needs the tensor-core
@@ -666,9 +673,12 @@ def head_norm_fw(X, weight, bias=None, *, eps: float = 1e-5, out: torch.Tensor |
     token-major for an output projection.  Returns ``(Y [B,T,NH*D], mean, rstd
     [B,NH,T] float32)``.  With NH = 1 it is the layer norm of B*T rows."""
     B, NH, T, D, dev, dt = _check_head_norm(X, weight, bias)
-    Y = torch.empty((B, T, NH * D), dtype=dt, device=dev) if out is None else out
-    _check_tensor("out", Y, dt, (B, T, NH * D), dev)
-    mean = torch.empty((B, NH, T), dtype=torch.float32, device=dev)
+    if out is None:
+        Y = X.new_empty((B, T, NH * D))
+    else:
+        Y = out
+        _check_tensor("out", Y, dt, (B, T, NH * D), dev)
+    mean = weight.new_empty((B, NH, T))
     rstd = torch.empty_like(mean)
     with _on(dev):
         st = _lib.lib().mlstm_head_norm_fw(_ptr(X), _ptr(weight), _ptr(bias), _ptr(Y), _ptr(mean),
@@ -676,6 +686,15 @@ def head_norm_fw(X, weight, bias=None, *, eps: float = 1e-5, out: torch.Tensor |
                                            _stream(dev))
     _lib.check(st, "mlstm_head_norm_fw")
     return Y, mean, rstd
+
+
+@functools.lru_cache(maxsize=1024)
+def _head_norm_workspace(B, NH, T, D, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.lib().mlstm_head_norm_bw_workspace_size(B, NH, T, D, _DT[dtype],
+                                                            ctypes.byref(n)),
+               "mlstm_head_norm_bw_workspace_size")
+    return max(int(n.value), 1)
 
 
 def head_norm_bw(X, dY, weight, mean, rstd, *, bias: bool = True):
@@ -689,11 +708,7 @@ def head_norm_bw(X, dY, weight, mean, rstd, *, bias: bool = True):
     out = {"dX": torch.empty_like(X), "dweight": torch.empty_like(weight)}
     if bias:
         out["dbias"] = torch.empty_like(weight)
-    n = ctypes.c_size_t(0)
-    _lib.check(_lib.lib().mlstm_head_norm_bw_workspace_size(B, NH, T, D, _DT[dt],
-                                                            ctypes.byref(n)),
-               "mlstm_head_norm_bw_workspace_size")
-    ws = torch.empty(max(n.value, 1), dtype=torch.uint8, device=dev)
+    ws = torch.empty(_head_norm_workspace(B, NH, T, D, dt), dtype=torch.uint8, device=dev)
     with _on(dev):
         st = _lib.lib().mlstm_head_norm_bw(
             _ptr(X), _ptr(dY), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(out["dX"]),
