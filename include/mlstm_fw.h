@@ -316,8 +316,7 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
                                   int DV, float scale, mlstm_dtype dtype, mlstm_algo algo,
                                   void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
 
-/* Training pair: mlstm_gated_delta_fw_train is the forward (AUTO's, same
- * results) that also keeps, in a caller buffer `saved`, what it formed per 128
+/* Training pair: mlstm_gated_delta_fw_train is the forward that also keeps, in a caller buffer `saved`, what it formed per 128
  * tokens (sums of g, inverses, transition matrices, states and y, about 2.1 KB
  * per token and head at DK = DV = 128); mlstm_gated_delta_bw_saved is
  * mlstm_gated_delta_bw from it, without recomputing the forward.  `saved` must

@@ -17,9 +17,11 @@ using namespace tc;
 // T21 = -T22 A21 T11 for the two 64-blocks at once and for the whole, on the
 // tensor cores with both operands as two bf16 terms (A21 and T22 in tensor
 // memory, T11 and A21 T11 as images).  A dozen dependent passes of little work
-// each, bound by their latency: three blocks share an SM (66 KB, 128
-// tensor-memory columns: K K^T, whose columns the operands [0, 64) and the
-// products [64, 128) take once A is in registers and shared memory).
+// each, bound by their latency and by the barriers between them: two blocks share
+// an SM (66 KB, 128 tensor-memory columns: K K^T, whose columns the operands
+// [0, 64) and the products [64, 128) take once A is in registers and shared
+// memory).  Three blocks (80 registers, which spill) took as long with 8192 chunks
+// (293 us) and longer with 512 (28.6 against 25.0 us).
 constexpr int kInvThreads = 256;
 constexpr int kLd = 36;                     // floats per row of a diagonal block
 constexpr uint32_t kBi = 8192;              // lo term of the products' images (64 rows)
@@ -32,7 +34,7 @@ constexpr uint32_t kISmem = kIBar + 64;
 
 // kT: also Tinv^T.
 template <bool kT>
-__global__ void __launch_bounds__(kInvThreads, 3)
+__global__ void __launch_bounds__(kInvThreads, 2)
 gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
                       const float* __restrict__ g, const float* __restrict__ beta, GdnTcWs w) {
   extern __shared__ __align__(1024) uint8_t smem[];

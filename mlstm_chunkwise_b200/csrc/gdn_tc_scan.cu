@@ -11,8 +11,8 @@
 //      P
 //   4  H = scale (Lam Q S + P y)   meanwhile the next state's image, e^G S
 // Four dependent rounds, 104 products of 128 x 128 x 16 (7300 cycles) and about as
-// long in passes: slower per chunk than the staged forward where few heads leave
-// SMs idle, see gdn_tc_fw_fused().
+// long in passes (11 us a chunk): behind the staged forward where few heads with
+// many chunks leave SMs idle, see gdn_tc_fw_fused().
 // Tensor memory: S [0, 128), X and y [128, 256), Tinv then Q K^T and P [256, 384),
 // Q S then H [384, 512).  Shared memory blocks: K 0, 1; Q 2, 3; V 4, 5; z, y, H 6..9;
 // D beta y, then the state's image 10..13.
@@ -300,11 +300,18 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 }  // namespace
 
-// A chunk costs a fused block about 7 us, the staged forward 19 us of one SM (mn
-// and out) and its recurrence 1.4 us: the fused one wins from about 48 (bh, pair
-// of value tiles) on, a third of the SMs.
+// By what the two cost in us, measured: a chunk takes a fused block 11; the staged
+// forward takes a wave of 148 (head, chunk, pair of value tiles) 21 (mn and out),
+// its recurrence 1.45 a chunk, and two more launches 5.  So the fused one runs for
+// one or two chunks, and from about half a wave of heads on.  (16 heads of 32
+// chunks: 135 staged, 352 fused; 256 heads: 1390 and 711.)
 bool gdn_tc_fw_fused(const GdnProblem& p) {
-  return (long)p.BH * ((p.DV + 127) / 128) >= 48;
+  const long nc = gdn_tc_chunks(p), heads = (long)p.BH * ((p.DV + 127) / 128);
+  auto waves = [](long n) { return (n + kGdnSms - 1) / kGdnSms; };
+  const long fused = 1100 * nc * waves(heads);
+  const long staged = 2100 * waves(heads * nc) +
+                      145 * nc * waves((long)p.BH * ((p.DV + 63) / 64)) + 500;
+  return fused <= staged;
 }
 
 cudaError_t launch_gdn_tc_scan(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m, float* C_T,
