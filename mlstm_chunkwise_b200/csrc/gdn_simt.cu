@@ -3,6 +3,11 @@
 // gdn.h, in chunks of 64 tokens.  Every product is a block-level tiled matrix
 // product whose operands are read through small functors (masks, decays and
 // ragged ends are applied on the way in), so sizes need no padding in memory.
+//
+// What does not depend on the state (Tinv, W = Tinv Lam K, U = Tinv V and their
+// counterparts of the gradients) is formed for all chunks in parallel, and so is
+// what follows from the states; only y = U - W S and S' = e^G S + K^T (D beta y)
+// run chunk after chunk.
 #include "gdn.h"
 
 namespace mlstm {
@@ -10,7 +15,6 @@ namespace {
 
 constexpr int kL = 64;        // chunk length
 constexpr int kThreads = 256;
-constexpr int kVT = 32;       // value columns per CTA of the sequential kernels
 constexpr int kKB = 32;       // depth of one staged slab of a product
 
 __host__ __device__ inline int chunks_of(int T) { return (T + kL - 1) / kL; }
@@ -325,13 +329,14 @@ gdn_simt_chunk(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
   }
 }
 
-// ---- the recurrences: one CTA per (bh, 32 value columns) ----------------
+// ---- the recurrences: one CTA per (bh, 16 kTN value columns) ------------
 // Forward: y = U - W S, S' = e^G S + K^T (D beta y).  Reverse: dz = dz0 + E dS',
 // dS = e^G dS' + Q^T (scale Lam dH) - K^T (Lam dz).
-template <typename T, bool kRev>
+template <typename T, bool kRev, int kTN>
 __global__ void __launch_bounds__(kThreads)
 gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ beta,
                const float* __restrict__ init, float* __restrict__ fin, T* __restrict__ dV, Ws w) {
+  constexpr int kVT = 16 * kTN;
   extern __shared__ float sh[];
   float *sa = sh, *sb = sa + kSa, *sy = sb + kSb;  // sy [64][33]
   float* sS = sy + 64 * 33;                        // [DK][33]
@@ -351,20 +356,20 @@ gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ 
     __syncthreads();
     load_gates(g, p, w, cb, beta, (long)bh * p.T + t0, n);
     const Rows<T> k{K + (kh * p.T + t0) * p.DK, n, p.DK};
-    float acc[4][2], add[4][2];
+    float acc[4][kTN], add[4][kTN];
     // what a product's result is added to is loaded ahead of the product
     for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 2; ++j) {
-        const int r = ty * 4 + i, v = v0 + tx * 2 + j;
+      for (int j = 0; j < kTN; ++j) {
+        const int r = ty * 4 + i, v = v0 + tx * kTN + j;
         add[i][j] = v < p.DV ? Y[(cb * kL + r) * p.DV + v] : 0.f;
       }
     zero(acc);
-    block_mm<2, true, false>(
+    block_mm<kTN, true, false>(
         acc, p.DK, [&](int m, int d) { return A[(cb * kL + m) * p.DK + d]; },
         [&](int d, int v) { return sS[d * 33 + v]; }, sa, sb);
     for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 2; ++j) {
-        const int r = ty * 4 + i, v = tx * 2 + j;
+      for (int j = 0; j < kTN; ++j) {
+        const int r = ty * 4 + i, v = tx * kTN + j;
         const float y = kRev ? add[i][j] + acc[i][j] : add[i][j] - acc[i][j];
         if (v0 + v < p.DV) {
           Y[(cb * kL + r) * p.DV + v0 + v] = y;
@@ -379,17 +384,17 @@ gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ 
     for (int d0 = 0; d0 < p.DK; d0 += 64) {
       if (kRev)
         for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 2; ++j) {
-            const int d = d0 + ty * 4 + i, v = v0 + tx * 2 + j;
+          for (int j = 0; j < kTN; ++j) {
+            const int d = d0 + ty * 4 + i, v = v0 + tx * kTN + j;
             add[i][j] = d < p.DK && v < p.DV ? St[(cb * p.DK + d) * p.DV + v] : 0.f;
           }
       zero(acc);
-      block_mm<2, false, false>(
+      block_mm<kTN, false, false>(
           acc, kL, [&](int m, int s) { return k(s, d0 + m); },
           [&](int s, int v) { return sy[s * 33 + v]; }, sa, sb);
       for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 2; ++j) {
-          const int d = d0 + ty * 4 + i, v = tx * 2 + j;
+        for (int j = 0; j < kTN; ++j) {
+          const int d = d0 + ty * 4 + i, v = tx * kTN + j;
           if (d >= p.DK) continue;
           const float old = sS[d * 33 + v];
           if (v0 + v < p.DV) St[(cb * p.DK + d) * p.DV + v0 + v] = old;
@@ -684,6 +689,23 @@ cudaError_t prep(const GdnProblem& p, const GdnInputs& x, const Ws& w, cudaStrea
   return cudaGetLastError();
 }
 
+// A recurrence is bound by the latency of its products (10 us a chunk of 128 x 32
+// state columns, an SM 9% busy), so that its columns are spread over twice the
+// blocks, 16 each, while those still find free SMs.
+template <typename T, bool kRev>
+cudaError_t chain(const GdnProblem& p, const GdnInputs& x, const float* init, float* fin, T* dV,
+                  const Ws& w, cudaStream_t st) {
+  auto go = [&](auto* kern, int cols) {
+    const cudaError_t e = allow(kern, chain_smem(p));
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((p.DV + cols - 1) / cols, p.BH), kThreads, chain_smem(p), st>>>(
+        p, (const T*)x.K, x.beta, init, fin, dV, w);
+    return cudaGetLastError();
+  };
+  if ((long)p.BH * ((p.DV + 15) / 16) <= 148) return go(&gdn_simt_chain<T, kRev, 1>, 16);
+  return go(&gdn_simt_chain<T, kRev, 2>, 32);
+}
+
 // prep and chunk quantities, then the forward recurrence
 template <typename T, bool kBw>
 cudaError_t states(const GdnProblem& p, const GdnInputs& x, const void* dH, float* C_T, const Ws& w,
@@ -694,10 +716,7 @@ cudaError_t states(const GdnProblem& p, const GdnInputs& x, const void* dH, floa
   gdn_simt_chunk<T, kBw><<<dim3(chunks_of(p.T), p.BH), kThreads, kChunkSmem, st>>>(
       p, (const T*)x.Q, (const T*)x.K, (const T*)x.V, x.beta, (const T*)dH, w);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = allow(gdn_simt_chain<T, false>, chain_smem(p))) != cudaSuccess) return e;
-  gdn_simt_chain<T, false><<<dim3((p.DV + kVT - 1) / kVT, p.BH), kThreads, chain_smem(p), st>>>(
-      p, (const T*)x.K, x.beta, x.C0, C_T, nullptr, w);
-  return cudaGetLastError();
+  return chain<T, false>(p, x, x.C0, C_T, nullptr, w, st);
 }
 
 template <typename T>
@@ -719,10 +738,7 @@ cudaError_t bw(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, void*
   const dim3 chunks(chunks_of(p.T), p.BH);
   cudaError_t e = states<T, true>(p, x, d.dH, nullptr, w, st);
   if (e != cudaSuccess) return e;
-  if ((e = allow(gdn_simt_chain<T, true>, chain_smem(p))) != cudaSuccess) return e;
-  gdn_simt_chain<T, true><<<dim3((p.DV + kVT - 1) / kVT, p.BH), kThreads, chain_smem(p), st>>>(
-      p, (const T*)x.K, x.beta, d.dC_T, d.dC0, (T*)d.dV, w);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = chain<T, true>(p, x, d.dC_T, d.dC0, (T*)d.dV, w, st)) != cudaSuccess) return e;
   if ((e = allow(gdn_simt_grads<T>, kGradSmem)) != cudaSuccess) return e;
   gdn_simt_grads<T><<<chunks, kThreads, kGradSmem, st>>>(p, (const T*)x.Q, (const T*)x.K, x.beta,
                                                          (const T*)d.dH, (T*)d.dQ, (T*)d.dK, d.dg,
