@@ -3,13 +3,15 @@
 // Per (bh, chunk, up to 128 value columns), from the state S entering the chunk:
 //   X = K S,  z = V - Lam X,  y = Tinv z,  H = scale (Lam Q S + P y),
 //   P_rs = Gam_rs beta_s q_r.k_s (s <= r)
-// Persistent, one block per SM.  Three rounds of products with a pass through registers after each:
-// {K S, Q S, Q K^T}, {Tinv z} under which P is formed, {P y}.  The next item's
-// tiles are copied in as soon as this one's have been read, and its Tinv waits in
-// registers.  88 products of 128 x 128 x 16 (about 6000
-// cycles) per 128 tokens and 240 KB of traffic; two blocks per SM on 64 columns
-// each with four rounds took three times as long (Tinv, Q, K and P twice, loads
-// exposed).
+// Persistent, one block per SM.  Three rounds of products with a pass through
+// registers after each: {K S, Q S, Q K^T}, under which Tinv goes to tensor memory;
+// {Tinv z}, under which P is formed; {P y}.  The next item's tiles are copied in as
+// soon as this one's have been read.  88 products of 128 x 128 x 16 (about 6000
+// cycles) and 230 KB of traffic per item.  1024 items: 78 us (82 with y kept), 11 us
+// an item, of which about 7 are products and passes; the rest waits for the next
+// tiles, although HBM runs at 2.9 TB/s and nothing is saturated (tensor pipe 22%,
+// issue slots 30%).  Two blocks per SM on 64 columns each with four rounds took
+// 101 us (Tinv, Q, K and P twice, loads exposed).
 // Tensor memory: Tinv [0, 128), Q K^T then P [128, 256), X, y, P y [256, 384),
 // Q S [384, 512).
 #include <cuda.h>

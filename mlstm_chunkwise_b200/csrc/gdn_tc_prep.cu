@@ -287,8 +287,11 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
 // ------------------------------------------------------------------ M and N
 // Per (bh, chunk, up to 128 value columns): two rounds,
 //   {W = (Tinv Lam) K, U = Tinv V}, {M = K^T (D beta W), N = K^T (D beta U)}.
-// 72 products of 128 x 128 x 16 (about 4900 cycles).  M only with the first pair
-// of value tiles.  Tensor memory: Tinv [0, 128), W then M [128, 256), U then N
+// 72 products of 128 x 128 x 16 (about 4900 cycles) and 230 KB of traffic per item.
+// M only with the first pair of value tiles.  The next item's Tinv and Tinv Lam are
+// put in place under the second round.  1024 items: 65 to 69 us, 9.8 us an item, of
+// which 7.5 are products and passes; the rest waits for the next K and V.
+// Tensor memory: Tinv [0, 128), W then M [128, 256), U then N
 // [256, 384), Tinv Lam [384, 512).
 constexpr uint32_t kMV = 2 * kBlk, kMW = 4 * kBlk, kMU = 8 * kBlk;
 constexpr uint32_t kMLam = 14 * kBlk;
