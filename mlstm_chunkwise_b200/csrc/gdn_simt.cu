@@ -420,7 +420,8 @@ gdn_simt_out(GdnProblem p, const T* __restrict__ Q, const float* __restrict__ be
   extern __shared__ float sh[];
   float *sa = sh, *sb = sa + kSa;
   Gates64* g = reinterpret_cast<Gates64*>(sb + kSb);
-  const int v0 = blockIdx.x * 64, c = blockIdx.y, bh = blockIdx.z, NC = gridDim.y;
+  // chunks along x: there may be more than the 65535 blocks that y holds
+  const int v0 = blockIdx.y * 64, c = blockIdx.x, bh = blockIdx.z, NC = gridDim.x;
   const int t0 = c * kL, n = min(kL, p.T - t0);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const size_t cb = (size_t)bh * NC + c;
@@ -728,7 +729,7 @@ cudaError_t fw(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T, voi
   cudaError_t e = states<T, false>(p, x, nullptr, C_T, w, st);
   if (e != cudaSuccess) return e;
   if ((e = allow(gdn_simt_out<T>, kOutSmem)) != cudaSuccess) return e;
-  gdn_simt_out<T><<<dim3((p.DV + 63) / 64, chunks_of(p.T), p.BH), kThreads, kOutSmem, st>>>(
+  gdn_simt_out<T><<<dim3(chunks_of(p.T), (p.DV + 63) / 64, p.BH), kThreads, kOutSmem, st>>>(
       p, (const T*)x.Q, x.beta, (T*)H, w);
   return cudaGetLastError();
 }

@@ -172,6 +172,35 @@ def test_padding_leaves_the_state(algo):
     check(algo, {"C": C}, {"C": ref.forward(**gd.fp64(cut))[1]})
 
 
+@pytest.mark.parametrize("kw", [dict(T=300), dict(T=100), dict(T=300, dtype="f32")], ids=str)
+def test_without_the_final_state(kw):
+    """H is the same bits whether or not the final state is asked for."""
+    x = gd.cuda(gd.make(DK=64, DV=96, **kw))
+    a = [x[n] for n in gd.NAMES]
+    H, _ = api.gated_delta_fw(*a)
+    assert torch.equal(H, api.gated_delta_fw(*a, return_last_state=False))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_longest_sequence(dtype):
+    """2^22 tokens: behind a reset near the end, a sequence of its own."""
+    T, n = 1 << 22, 300
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    mk = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    q, k = (torch.nn.functional.normalize(mk(1, 1, T, 8), dim=-1).to(gd.DT[dtype])
+            for _ in range(2))
+    v = mk(1, 1, T, 8).to(gd.DT[dtype])
+    g, beta = -0.1 * mk(1, 1, T).abs(), torch.sigmoid(mk(1, 1, T))
+    g[:, :, T - n] = float("-inf")
+    x = dict(zip(gd.NAMES, (q, k, v, g, beta, None)))
+    H, C = api.gated_delta_fw(q, k, v, g, beta)
+    tail = {m: None if t is None else t[:, :, T - n:].cpu() for m, t in x.items()}
+    H64, C64 = ref.forward(**gd.fp64(tail))
+    check("simt" if dtype == "f32" else "tc", {"H": H[:, :, T - n:], "C": C},
+          {"H": H64, "C": C64})
+    assert torch.isfinite(H).all()
+
+
 def test_zero_length():
     x = gd.cuda(gd.make(T=0))
     H, C = api.gated_delta_fw(*(x[n] for n in gd.NAMES))
