@@ -45,7 +45,8 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   float* sbeta = reinterpret_cast<float*>(smem + kOffBeta);
   float* scol = reinterpret_cast<float*>(smem + kOffCol);
   const uint32_t qa = sbase + kOffQ, ka = sbase + kOffK, sa = sbase + kOffS, za = sbase + kOffZ;
-  const uint32_t bar_in = sbase + kOffBar, bar_v = bar_in + 8;
+  // bar_f: what the image held (y or H of the item before) has left
+  const uint32_t bar_in = sbase + kOffBar, bar_v = bar_in + 8, bar_f = bar_in + 24;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
@@ -82,7 +83,7 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   GdnItem x(blockIdx.x, p, w);
   gdn_next_stage();
   if (lead) {
-    for (int i = 0; i < 3; ++i) mbar_init(bar_in + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar_in + 8 * i, 1);
     fence_barrier_init();
     load_v(x);
     load_tiles(x, true);
@@ -118,7 +119,6 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
       load_tinv(w.tinv + x.cb * 32 * 128, r, h, h <= q, ti);  // for the second round
     }
-    if (lead) tma_store_wait_read_all();  // what the image held has left
     gdn_round(
         rd, 0x61,
         [&] {
@@ -138,8 +138,12 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           put_tinv(tlane, h, ti);
           if (more) load_gates(nx);
           if (rd.ok) rd.ok = mbar_wait(bar_v, in_phase, rd.wt, 0x65);
+          if (rd.ok) rd.ok = mbar_wait(bar_f, in_phase, rd.wt, 0x66);
         },
-        gdn_nothing,
+        [&] {
+          tma_store_wait_read_all();
+          mbar_arrive(bar_f);
+        },
         [&] {
           if (more) load_tiles(nx, false);
         });

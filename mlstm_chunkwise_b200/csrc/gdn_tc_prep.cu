@@ -306,7 +306,8 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const uint32_t sbase = smem_u32(smem);
   float* slam = reinterpret_cast<float*>(smem + kMLam);
   const uint32_t ka = sbase, va = sbase + kMV, wa = sbase + kMW, ua = sbase + kMU;
-  const uint32_t bar_k = sbase + kMBar, bar_v = bar_k + 8;
+  // bar_f: M of the item before has left the image
+  const uint32_t bar_k = sbase + kMBar, bar_v = bar_k + 8, bar_f = bar_k + 24;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kMBar + 32);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
@@ -337,7 +338,7 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   GdnItem x(blockIdx.x, p, w);
   gdn_next_stage();
   if (lead) {
-    for (int i = 0; i < 3; ++i) mbar_init(bar_k + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar_k + 8 * i, 1);
     fence_barrier_init();
     load_k(x);
     load_v(x);
@@ -394,7 +395,6 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t nv = idesc_bf16(128, x.tiles * 64, 0, 1),
                    nvt = idesc_bf16(128, x.tiles * 64, 1, 1);
     const float dec = row ? nbt * gdn_decay(ngl, ngc) : 0.f;
-    if (lead) tma_store_wait_read_all();  // M of the item before has left
     gdn_round(
         rd, 0x47,
         [&] {
@@ -407,8 +407,12 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         },
         [&] {
           if (more) load_rows(nx);
+          if (rd.ok) rd.ok = mbar_wait(bar_f, in_phase, rd.wt, 0x4c);
         },
-        gdn_nothing,
+        [&] {
+          tma_store_wait_read_all();
+          mbar_arrive(bar_f);
+        },
         [&] {
           if (more) load_v(nx);
         });

@@ -6,12 +6,11 @@
 //   1  X = K S, Q S           meanwhile Tinv to tensor memory
 //      z = V - Lam X
 //   2  y = Tinv z             meanwhile Q S is scaled in place
-//      the images of y and of D beta y
-//   3  S = e^G S + K^T (D beta y), Q K^T
-//      P
+//      the image of D beta y
+//   3  Q K^T, S = e^G S + K^T (D beta y)   meanwhile the image of y, then P
 //   4  H = scale (Lam Q S + P y)   meanwhile the next state's image, e^G S
 // Four dependent rounds, 104 products of 128 x 128 x 16 (7300 cycles) and about as
-// long in passes (11 us a chunk): behind the staged forward where few heads with
+// long in passes (10.5 us a chunk): behind the staged forward where few heads with
 // many chunks leave SMs idle, see gdn_tc_fw_fused().
 // Tensor memory: S [0, 128), X and y [128, 256), Tinv then Q K^T and P [256, 384),
 // Q S then H [384, 512).  Shared memory blocks: K 0, 1; Q 2, 3; V 4, 5; z, y, H 6..9;
@@ -47,8 +46,10 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
   float* scol = reinterpret_cast<float*>(smem + kOffCol);
   const uint32_t ka = sbase, qa = sbase + kOffQ, va = sbase + kOffV, za = sbase + kOffZ,
                  ua = sbase + kOffU;
-  const uint32_t bar_qk = sbase + kOffBar, bar_v = bar_qk + 8;
-  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 32);
+  // bar_p: Q K^T has been formed; bar_h: H has left the image
+  const uint32_t bar_qk = sbase + kOffBar, bar_v = bar_qk + 8, bar_p = bar_qk + 24,
+                 bar_h = bar_qk + 32;
+  volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 48);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
   const bool row = tid < kGdnRows, lead = tid == kGdnRows;
@@ -81,7 +82,7 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
   };
 
   if (lead) {
-    for (int i = 0; i < 3; ++i) mbar_init(bar_qk + 8 * i, 1);
+    for (int i = 0; i < 5; ++i) mbar_init(bar_qk + 8 * i, 1);
     fence_barrier_init();
     load_qk(0);
     load_v(0);
@@ -159,8 +160,14 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
           put_tinv(tlane + 256, h, ti);
           if (more) load_gates(c + 1);
           if (rd.ok) rd.ok = mbar_wait(bar_v, ph, rd.wt, 0x85);
+          if (c > 0 && rd.ok) rd.ok = mbar_wait(bar_h, ph ^ 1, rd.wt, 0x86);
         },
-        gdn_nothing, gdn_nothing);
+        [&] {
+          if (c == 0) return;
+          tma_store_wait_read_all();
+          mbar_arrive(bar_h);
+        },
+        gdn_nothing);
     if (cols) {
       tmem_ld32(trow + 128, v);
       tmem_wait_ld();
@@ -197,10 +204,7 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (int cc = 0; cc < 4; ++cc) {
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[8 * cc + e]);
-        put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= dec;
+        for (int e = 0; e < 8; ++e) y[e] = dec * __uint_as_float(v[8 * cc + e]);
         put8(imgu, 2 * kBlk, r, (h & 1) * 4 + cc, y);
       }
     }
@@ -208,42 +212,53 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
         rd, 0x83,
         [&] {
           mma_ss<false, false>(tmem + 256, qa, ka, idesc_bf16(128, 128, 0, 0), slabs, true);
+          mma_commit(bar_p);
           for (int t = 0; t < 2; ++t)
             mma_ss<true, true>(tmem, ka, ua + 2 * t * kBlk, idt, 2, false);
         },
-        gdn_nothing, gdn_nothing,
+        [&] {
+          if (cols) {
+            tmem_ld32(trow + 128, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc)
+              put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
+          }
+          // P: 32 keys of the row; its terms take the scores' columns, hi then lo
+          if (rd.ok) rd.ok = mbar_wait(bar_p, ph, rd.wt, 0x87);
+          tc_fence_after();
+          uint32_t hi[16], lo[16];
+          if (h <= q) {
+            tmem_ld32(trow + 256, v);
+            tmem_wait_ld();
+            float s[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = p.scale * __uint_as_float(v[e]);
+            if (h == q && gc[h * 32].x - gc[h * 32 + 31].x > kGdnFlat) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int k = h * 32 + e;
+                s[e] = e <= lane ? gdn_decay(gr, gc[k]) * sbeta[k] * s[e] : 0.f;
+              }
+            } else {
+              const bool d = h == q;
+              const float f = gdn_decay(gr, gc[h * 32 + (d ? 0 : 31)]);
+              const float* sc = scol + (d ? 128 : 0) + h * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] = d && e > lane ? 0.f : s[e] * (f * sc[e]);
+            }
+            split_pack<32>(s, hi, lo);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
+          }
+          tmem_st16(trow + 256, hi);
+          tmem_st16(trow + 272, lo);
+        },
+        gdn_nothing,
         [&] {
           if (more) load_qk(c + 1);
         });
-    if (row) {  // P: 32 keys of the row; its terms take the scores' columns, hi then lo
-      uint32_t hi[16], lo[16];
-      if (h <= q) {
-        tmem_ld32(trow + 256, v);
-        tmem_wait_ld();
-        float s[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] = p.scale * __uint_as_float(v[e]);
-        if (h == q && gc[h * 32].x - gc[h * 32 + 31].x > kGdnFlat) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int k = h * 32 + e;
-            s[e] = e <= lane ? gdn_decay(gr, gc[k]) * sbeta[k] * s[e] : 0.f;
-          }
-        } else {
-          const bool d = h == q;
-          const float f = gdn_decay(gr, gc[h * 32 + (d ? 0 : 31)]);
-          const float* sc = scol + (d ? 128 : 0) + h * 32;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = d && e > lane ? 0.f : s[e] * (f * sc[e]);
-        }
-        split_pack<32>(s, hi, lo);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
-      }
-      tmem_st16(trow + 256, hi);
-      tmem_st16(trow + 272, lo);
-    }
     gdn_round(
         rd, 0x84,
         [&] {
@@ -287,7 +302,6 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (int t = 0; t < tiles; ++t)
         tma_store_3d(&tm_h, za + t * kBlk, (vt + t) * 64, c * kGdnL, bh);
       tma_store_commit();
-      tma_store_wait_read_all();  // before z takes its place, behind the next round
     }
   }
   if (lead) tma_store_wait_all();
@@ -300,11 +314,11 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 }  // namespace
 
-// By what the two cost in us, measured: a chunk takes a fused block 11; the staged
+// By what the two cost in us, measured: a chunk takes a fused block 10.5 to 11; the staged
 // forward takes a wave of 148 (head, chunk, pair of value tiles) 21 (mn and out),
 // its recurrence 1.45 a chunk, and two more launches 5.  So the fused one runs for
 // one or two chunks, and from about half a wave of heads on.  (16 heads of 32
-// chunks: 135 staged, 352 fused; 256 heads: 1390 and 711.)
+// chunks: 135 staged, 352 fused; 256 heads: 1390 and 675.)
 bool gdn_tc_fw_fused(const GdnProblem& p) {
   const long nc = gdn_tc_chunks(p), heads = (long)p.BH * ((p.DV + 127) / 128);
   auto waves = [](long n) { return (n + kGdnSms - 1) / kGdnSms; };
