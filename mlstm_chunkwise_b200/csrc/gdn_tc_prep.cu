@@ -11,26 +11,33 @@ namespace {
 using namespace tc;
 
 // ------------------------------------------------------------------ inverse
-// One block of 256 threads per (bh, chunk), thread (r, h) on one of two column
-// halves of row r.  The inverse goes by blocks: the four 32 x 32 diagonal blocks
-// by forward substitution in fp32 (a warp per block, a lane per column); then
-// T21 = -T22 A21 T11 for the two 64-blocks at once and for the whole, on the
-// tensor cores with both operands as two bf16 terms (A21 and T22 in tensor
-// memory, T11 and A21 T11 as images).  A dozen dependent passes of little work
-// each, bound by their latency and by the barriers between them: two blocks share
-// an SM (66 KB, 128 tensor-memory columns: K K^T, whose columns the operands
-// [0, 64) and the products [64, 128) take once A is in registers and shared
-// memory).  Three blocks (80 registers, which spill) took as long with 8192 chunks
-// (293 us) and longer with 512 (28.6 against 25.0 us).
+// Persistent, blocks of 256 threads, thread (r, h) on one of two column halves of
+// row r.  The inverse goes by blocks: the four 32 x 32 diagonal blocks by forward
+// substitution in fp32 (a warp per block, a lane per column), while the other warps
+// form the terms of A left of them; then T21 = -T22 A21 T11 for the two 64-blocks
+// at once and for the whole, on the tensor cores with both operands as two bf16
+// terms (A21 and T22 in tensor memory, T11 and A21 T11 as images).  Half a dozen
+// dependent passes of little work each, bound by their latency: two blocks share
+// an SM, and the next item's K, its K K^T and its sums are prepared meanwhile
+// (8192 chunks 208 us, 512 chunks 21; a block per item 262 and 22).  What costs
+// beyond that is instruction fetch, so loops whose copies would differ in little
+// stay rolled, and anything in local memory, for which the shared memory leaves
+// little L1 (a row's diagonal bit cleared by index, not by mask: 293 us).
+// Tensor memory: operands [0, 64), products [64, 128), K K^T [128, 256), where the
+// terms of A21 of the whole take the columns that they came from.
 constexpr int kInvThreads = 256;
 constexpr int kLd = 36;                     // floats per row of a diagonal block
 constexpr uint32_t kBi = 8192;              // lo term of the products' images (64 rows)
-constexpr uint32_t kIDiag = kBlk;           // float[4][32][kLd]
-constexpr uint32_t kIGc = 4 * kBlk;
-constexpr uint32_t kIBeta = kIGc + 1024;
-constexpr uint32_t kICol = kIBeta + 512;    // float[2][128]: beta times the column's factor
-constexpr uint32_t kIBar = kICol + 1024;
-constexpr uint32_t kISmem = kIBar + 64;
+// behind K twice (this item's, the next one's): float2[128] sums, beta, and
+// float[2][128], beta times the column's factor
+constexpr uint32_t kIGates = 2 * kBlk, kIGate = 1024 + 512 + 1024;
+constexpr uint32_t kIBar = kIGates + 2 * kIGate;
+constexpr uint32_t kIWork = kIGates + 6 * 1024;  // the products' image; with kT Tinv in the end
+constexpr uint32_t kIDiag = kIWork + kBlk;       // float[4][32][kLd]
+constexpr uint32_t inv_smem(bool kT) {
+  return kT ? kIWork + 4 * kBlk : kIDiag + 4 * 32 * kLd * 4;
+}
+static_assert(2 * (inv_smem(true) + 1024) <= 228 * 1024, "two blocks per SM");
 
 // kT: also Tinv^T.
 template <bool kT>
@@ -39,248 +46,279 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
                       const float* __restrict__ g, const float* __restrict__ beta, GdnTcWs w) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  float2* gc = reinterpret_cast<float2*>(smem + kIGc);
-  float* sbeta = reinterpret_cast<float*>(smem + kIBeta);
-  float* scol = reinterpret_cast<float*>(smem + kICol);
-  const uint32_t bar_k = sbase + kIBar, bar = bar_k + 8;
+  const uint32_t bar_k = sbase + kIBar, bar_kk = bar_k + 8, bar = bar_k + 16;
   volatile uint32_t* slot = reinterpret_cast<volatile uint32_t*>(smem + kIBar + 32);
-  const int c = blockIdx.x, bh = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
-  const int t0 = c * kGdnL, n = min(kGdnL, p.T - t0);
   const int slabs = (p.DK + 63) / 64;
-  const size_t cb = (size_t)bh * w.NC + c;
+  const int items = p.BH * w.NC;  // each has 160 KB of workspace or more: an int holds them
   const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
-
-  gdn_next_stage();
-  if (tid == 0) {
-    mbar_init(bar_k, 1);
-    mbar_init(bar, 1);
-    fence_barrier_init();
+  // item i: chunk i % NC of head i / NC, so rows i * 128 of the workspace's arrays
+  auto load_k = [&](int i) {
+    const int bh = i / w.NC, t0 = (i - bh * w.NC) * kGdnL;
     mbar_expect_tx(bar_k, slabs * kBlk);
     for (int s = 0; s < slabs; ++s)
       tma_load_3d(sbase + s * kBlk, &tm_k, s * 64, t0, gdn_key_head(p, bh), bar_k);
+  };
+  auto put_gates = [&](int i, uint32_t buf) {  // by one warp
+    const int bh = i / w.NC, t0 = (i - bh * w.NC) * kGdnL, n = min(kGdnL, p.T - t0);
+    const long at = (long)bh * p.T + t0;
+    float2* gc = reinterpret_cast<float2*>(smem + kIGates + buf * kIGate);
+    float* sbeta = reinterpret_cast<float*>(gc + 128);
+    float bt[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) bt[b] = b * 32 + lane < n ? beta[at + b * 32 + lane] : 0.f;
+    gdn_chunk_sums(g + at, n, lane, gc, w.gc + (size_t)i * kGdnL);
+    __syncwarp();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int t = b * 32 + lane;
+      const float2 gt = gc[t];
+      sbeta[t] = bt[b];
+      sbeta[128 + t] = bt[b] * gdn_col_factor(gt, 31);
+      sbeta[256 + t] = __fdividef(bt[b], gdn_col_factor(gt, 0));
+    }
+  };
+
+  gdn_next_stage();
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(bar_k + 8 * i, 1);
+    fence_barrier_init();
+    load_k(blockIdx.x);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32((const void*)slot), 128);
+    tmem_alloc(smem_u32((const void*)slot), 256);
     tmem_relinquish();
   }
-  if (warp == 2) gdn_chunk_sums(g + (long)bh * p.T + t0, n, lane, gc, w.gc + cb * kGdnL);
-  if (warp >= 4) {
-    const int t = tid - 128;
-    sbeta[t] = t < n ? beta[(long)bh * p.T + t0 + t] : 0.f;
-  }
+  if (warp == 4) put_gates(blockIdx.x, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
   const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
   bool ok = true;
-  uint32_t phase = 0;
-  if (warp >= 4) {
-    scol[r] = sbeta[r] * gdn_col_factor(gc[r], 31);
-    scol[128 + r] = __fdividef(sbeta[r], gdn_col_factor(gc[r], 0));
-  }
-
-  run_mma(bar, phase, ok, wt, 0x42, [&] {
-    ok = mbar_wait(bar_k, 0, wt, 0x41);
+  uint32_t phase = 0, ph = 0;
+  auto k_product = [&](uint32_t k_phase) {  // by one lane
+    if (ok) ok = mbar_wait(bar_k, k_phase, wt, 0x41);
     tc_fence_after();
-    if (ok) mma_ss<false, false>(tmem, sbase, sbase, idesc_bf16(128, 128, 0, 0), slabs, true);
-  });
-  const float2 gr = gc[r];
-  // the terms of block b (columns 32 b ..) of A's row r, left of the diagonal's
-  auto a_block = [&](int b, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-    uint32_t v[32];
-    tmem_ld32(trow + b * 32, v);
-    tmem_wait_ld();
-    const float f = gdn_decay(gr, gc[b * 32 + 31]);
-    float x[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = f * scol[b * 32 + e] * __uint_as_float(v[e]);
-    split_pack<32>(x, hi, lo);
+    if (ok) mma_ss<false, false>(tmem + 128, sbase, sbase, idesc_bf16(128, 128, 0, 0), slabs, true);
+    mma_commit(bar_kk);
   };
+  if (warp == 0 && elect_one()) k_product(0);
+  __syncwarp();
+
   float* diag = reinterpret_cast<float*>(smem + kIDiag);
   float* dq = diag + q * 32 * kLd;  // [s][r] of block q
-  uint32_t hi1[16], lo1[16];        // A21 of the whole, columns 32 h ..
-  uint32_t hi0[16], lo0[16];        // A21 of the 64-blocks
-  if (q >= 2) a_block(h, hi1, lo1);
-  if (h == 0) {
-    uint32_t v[32];
-    tmem_ld32(trow + q * 32, v);
-    tmem_wait_ld();
-    if (gc[q * 32].x - gc[q * 32 + 31].x > kGdnFlat) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int s = q * 32 + e;
-        dq[e * kLd + lane] =
-            e < lane ? gdn_decay(gr, gc[s]) * sbeta[s] * __uint_as_float(v[e]) : 0.f;
-      }
-    } else {
-      const float f = gdn_decay(gr, gc[q * 32]);
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        dq[e * kLd + lane] =
-            e < lane ? f * scol[128 + q * 32 + e] * __uint_as_float(v[e]) : 0.f;
-    }
-  } else if (q & 1) {
-    a_block(q - 1, hi0, lo0);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (h == 0) {
-    // column `lane` of the block's inverse: once x_s is known its multiples leave
-    // all later rows (independent products)
-    float x[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = i == lane ? 1.f : 0.f;
-#pragma unroll
-    for (int s = 0; s < 31; ++s) {
-#pragma unroll
-      for (int r4 = (s + 1) / 4; r4 < 8; ++r4) {
-        const float4 v = *reinterpret_cast<const float4*>(dq + s * kLd + r4 * 4);
-        const float a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * r4 + i > s) x[4 * r4 + i] = fmaf(-a[i], x[s], x[4 * r4 + i]);
-      }
-    }
-    __syncwarp();  // every lane has read the block
-#pragma unroll
-    for (int r4 = 0; r4 < 8; ++r4)
-      *reinterpret_cast<float4*>(dq + lane * kLd + r4 * 4) =
-          make_float4(x[4 * r4], x[4 * r4 + 1], x[4 * r4 + 2], x[4 * r4 + 3]);
-  } else if (q & 1) {
-    // inner columns 0..31 are the first 64-block's, 32..63 the second's
-    const int at = q == 3 ? 16 : 0;
-    tmem_st16(trow + at, hi0);
-    tmem_st16(trow + 32 + at, lo0);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) hi0[e] = 0u;
-    tmem_st16(trow + 16 - at, hi0);
-    tmem_st16(trow + 48 - at, hi0);
-  }
-  __syncthreads();
-  // the image's rows: 0..31 and 32..63 are those of diagonal blocks 0 and 2
-  {
-    const int kr = tid & 63, cc = tid >> 6;
-    const float* d = diag + (kr >> 5) * 2 * 32 * kLd;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = d[(8 * cc + e) * kLd + (kr & 31)];
-    put8(smem, kBi, kr, cc, x);
-    put8(smem, kBi, kr, cc + 4, x);  // columns 32..63 of the product are not used
-  }
-  auto inv_mma = [&] {
+  uint8_t* img = smem + kIWork;
+  const uint32_t ia = sbase + kIWork;
+  auto inv_mma = [&](uint32_t a) {
     constexpr uint32_t id = idesc_bf16(128, 64, 0, 1);
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 3; ++t)
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ts(tmem + 64, tmem + (t == 1 ? 32 : 0) + kk * 8,
-                    mnmaj(sbase + (t == 2 ? kBi : 0u), kk), id, (t | kk) != 0);
+        mma_bf16_ts(tmem + 64, a + (kk >> 1) * 32 + (t == 1 ? 16 : 0) + (kk & 1) * 8,
+                    mnmaj(ia + (t == 2 ? kBi : 0u), kk), id, (t | kk) != 0);
   };
-  run_mma(bar, phase, ok, wt, 0x43, inv_mma);
-  if (q & 1) {
-    uint32_t v[16];
-    tmem_ld16(trow + 64 + h * 16, v);
-    tmem_wait_ld();
-    const int kr = (q >> 1) * 32 + lane;
-    put8(smem, kBi, kr, h * 2, reinterpret_cast<const float*>(v));
-    put8(smem, kBi, kr, h * 2 + 1, reinterpret_cast<const float*>(v) + 8);
-    float x[16];
+
+  for (int i = blockIdx.x; i < items; i += gridDim.x, ph ^= 1) {
+    const bool more = i + gridDim.x < items;
+    if (ok) ok = mbar_wait(bar_kk, ph, wt, 0x42);
+    tc_fence_after();
+    if (more && ok && tid == 128) load_k(i + gridDim.x);  // K has been read
+    const float2* gc = reinterpret_cast<const float2*>(smem + kIGates + ph * kIGate);
+    const float* sbeta = reinterpret_cast<const float*>(gc + 128);
+    const float* scol = sbeta + 128;
+    const float2 gr = gc[r];
+    if (h == 0) {
+      uint32_t v[32];
+      tmem_ld32(trow + 128 + q * 32, v);
+      tmem_wait_ld();
+      if (gc[q * 32].x - gc[q * 32 + 31].x > kGdnFlat) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = dq[(h * 16 + e) * kLd + lane];
-    uint32_t hi[8], lo[8];
-    split_pack<16>(x, hi, lo);
-    tmem_st8(trow + (q >> 1) * 16 + h * 8, hi);
-    tmem_st8(trow + 32 + (q >> 1) * 16 + h * 8, lo);
-  }
-  run_mma(bar, phase, ok, wt, 0x44, inv_mma);
-  // x: columns 32 h .. of this row inside its 64-block of the inverse
-  float x[32];
-  if (h == 0 && (q & 1)) {
-    uint32_t v[32];
-    tmem_ld32(trow + 64, v);
-    tmem_wait_ld();
+        for (int e = 0; e < 32; ++e) dq[e * kLd + lane] = __uint_as_float(v[e]);
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) {
+          const int s = q * 32 + e;
+          float* x = dq + e * kLd + lane;
+          *x = e < lane ? gdn_decay(gr, gc[s]) * sbeta[s] * *x : 0.f;
+        }
+      } else {
+        const float f = gdn_decay(gr, gc[q * 32]);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = -__uint_as_float(v[e]);
-  } else if (h == (q & 1)) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = dq[e * kLd + lane];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = 0.f;
-  }
-  if (q < 2) {
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc) put8(smem, kBi, r, h * 4 + cc, x + 8 * cc);
-  } else {
-    tmem_st16(trow + h * 16, hi1);
-    tmem_st16(trow + 32 + h * 16, lo1);
-  }
-  run_mma(bar, phase, ok, wt, 0x45, inv_mma);
-  split_pack<32>(x, hi1, lo1);
-  if (q >= 2) {
-    uint32_t v[32];
-    tmem_ld32(trow + 64 + h * 32, v);
-    tmem_wait_ld();
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc)
-      put8(smem, kBi, r - 64, h * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
-    tmem_st16(trow + h * 16, hi1);
-    tmem_st16(trow + 32 + h * 16, lo1);
-  }
-  run_mma(bar, phase, ok, wt, 0x46, inv_mma);
-  // the row's terms, without the identity: block b holds columns 32 b ..
-  uint4* dst = w.tinv + cb * 32 * 128 + r;
-  auto put_row = [&](int b, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-    if (b == q)  // the diagonal's one sits in hi
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (e == lane >> 1) hi[e] &= lane & 1 ? 0x0000ffffu : 0xffff0000u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 uh = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-      const uint4 ul = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-      if (b <= q) {
-        dst[(b * 4 + i) * 128] = uh;
-        dst[(16 + b * 4 + i) * 128] = ul;
+        for (int e = 0; e < 32; ++e)
+          dq[e * kLd + lane] =
+              e < lane ? f * scol[128 + q * 32 + e] * __uint_as_float(v[e]) : 0.f;
       }
-      if (kT) {
-        const uint32_t off = (b >> 1) * kBlk + sw128_offset(r, (b & 1) * 4 + i);
-        *reinterpret_cast<uint4*>(smem + off) = uh;
-        *reinterpret_cast<uint4*>(smem + 2 * kBlk + off) = ul;
+      __syncwarp();
+      // column `lane` of the block's inverse: once x_s is known its multiples leave
+      // all later rows (independent products)
+      float x[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = e == lane ? 1.f : 0.f;
+#pragma unroll
+      for (int s = 0; s < 31; ++s) {
+#pragma unroll
+        for (int r4 = (s + 1) / 4; r4 < 8; ++r4) {
+          const float4 v = *reinterpret_cast<const float4*>(dq + s * kLd + r4 * 4);
+          const float a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (4 * r4 + e > s) x[4 * r4 + e] = fmaf(-a[e], x[s], x[4 * r4 + e]);
+        }
+      }
+      __syncwarp();  // every lane has read the block
+#pragma unroll
+      for (int r4 = 0; r4 < 8; ++r4)
+        *reinterpret_cast<float4*>(dq + lane * kLd + r4 * 4) =
+            make_float4(x[4 * r4], x[4 * r4 + 1], x[4 * r4 + 2], x[4 * r4 + 3]);
+    } else if (q == 0) {
+      if (more) put_gates(i + gridDim.x, ph ^ 1);
+    } else {
+      // Blocks of A's rows left of the diagonal's (columns 32 b ..), as terms: for
+      // odd q that of A21 of the 64-blocks (inner columns 0..31 are the first one's,
+      // 32..63 the second's), for q >= 2 the two of A21 of the whole, in place.
+#pragma unroll 1
+      for (int j = q & 1 ? 0 : 1; j < (q >= 2 ? 3 : 1); ++j) {
+        const int b = j ? j - 1 : q - 1;
+        uint32_t v[32], hi[16], lo[16];
+        tmem_ld32(trow + 128 + b * 32, v);
+        tmem_wait_ld();
+        const float f = gdn_decay(gr, gc[b * 32 + 31]);
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = f * scol[b * 32 + e] * __uint_as_float(v[e]);
+        split_pack<32>(x, hi, lo);
+        const uint32_t to = trow + (j ? 128 + b * 32 : (q >> 1) * 32);
+        tmem_st16(to, hi);
+        tmem_st16(to + 16, lo);
+        if (j == 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0u;
+          tmem_st32(trow + 32 - (q >> 1) * 32, v);
+        }
       }
     }
-  };
-  put_row((q >> 1) * 2 + h, hi1, lo1);
-  if (q >= 2) {
-    uint32_t v[32];
-    tmem_ld32(trow + 64 + h * 32, v);
-    tmem_wait_ld();
+    __syncthreads();
+    // the image's rows: 0..31 and 32..63 are those of diagonal blocks 0 and 2
+    {
+      const int kr = tid & 63, cc = tid >> 6;
+      const float* d = diag + (kr >> 5) * 2 * 32 * kLd;
+      float x[8];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] ^= 0x80000000u;
-    split_pack<32>(reinterpret_cast<const float*>(v), hi1, lo1);
-    put_row(h, hi1, lo1);
+      for (int e = 0; e < 8; ++e) x[e] = d[(8 * cc + e) * kLd + (kr & 31)];
+      put8(img, kBi, kr, cc, x);
+      put8(img, kBi, kr, cc + 4, x);  // columns 32..63 of the product are not used
+    }
+    run_mma(bar, phase, ok, wt, 0x43, [&] { inv_mma(tmem); });
+    if (q & 1) {
+      uint32_t v[16];
+      tmem_ld16(trow + 64 + h * 16, v);
+      tmem_wait_ld();
+      const int kr = (q >> 1) * 32 + lane;
+      put8(img, kBi, kr, h * 2, reinterpret_cast<const float*>(v));
+      put8(img, kBi, kr, h * 2 + 1, reinterpret_cast<const float*>(v) + 8);
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = dq[(h * 16 + e) * kLd + lane];
+      uint32_t hi[8], lo[8];
+      split_pack<16>(x, hi, lo);
+      tmem_st8(trow + (q >> 1) * 32 + h * 8, hi);
+      tmem_st8(trow + (q >> 1) * 32 + 16 + h * 8, lo);
+    }
+    run_mma(bar, phase, ok, wt, 0x44, [&] { inv_mma(tmem); });
+    // x: columns 32 h .. of this row inside its 64-block of the inverse
+    float x[32];
+    if (h == 0 && (q & 1)) {
+      uint32_t v[32];
+      tmem_ld32(trow + 64, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = -__uint_as_float(v[e]);
+    } else if (h == (q & 1)) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = dq[e * kLd + lane];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = 0.f;
+    }
+    if (q < 2) {
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) put8(img, kBi, r, h * 4 + cc, x + 8 * cc);
+    }
+    run_mma(bar, phase, ok, wt, 0x45, [&] { inv_mma(tmem + 128); });
+    uint32_t hi[16], lo[16];
+    split_pack<32>(x, hi, lo);
+    if (q >= 2) {
+      uint32_t v[32];
+      tmem_ld32(trow + 64 + h * 32, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc)
+        put8(img, kBi, r - 64, h * 4 + cc, reinterpret_cast<const float*>(v) + 8 * cc);
+      tmem_st16(trow + h * 32, hi);
+      tmem_st16(trow + h * 32 + 16, lo);
+    }
+    run_mma(bar, phase, ok, wt, 0x46, [&] { inv_mma(tmem); });
+    if (more) {
+      if (warp == 0 && elect_one()) k_product(ph ^ 1);
+      __syncwarp();
+    }
+    // the row's terms, without the identity, by blocks (columns 32 b ..): that of
+    // its 64-block of the inverse, and for q >= 2 that of T21 of the whole
+    uint4* dst = w.tinv + (size_t)i * 32 * 128 + r;
+#pragma unroll 1
+    for (int j = 0; j < (q >= 2 ? 2 : 1); ++j) {
+      const int b = j ? h : (q >> 1) * 2 + h;
+      if (j) {
+        uint32_t v[32];
+        tmem_ld32(trow + 64 + h * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] ^= 0x80000000u;
+        split_pack<32>(reinterpret_cast<const float*>(v), hi, lo);
+      }
+      if (b == q) {  // the diagonal's one sits in hi
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          hi[e] &= e != lane >> 1 ? 0xffffffffu : lane & 1 ? 0x0000ffffu : 0xffff0000u;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 uh = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+        const uint4 ul = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+        if (b <= q) {
+          dst[(b * 4 + k) * 128] = uh;
+          dst[(16 + b * 4 + k) * 128] = ul;
+        }
+        if (kT) {
+          const uint32_t off = (b >> 1) * kBlk + sw128_offset(r, (b & 1) * 4 + k);
+          *reinterpret_cast<uint4*>(img + off) = uh;
+          *reinterpret_cast<uint4*>(img + 2 * kBlk + off) = ul;
+        }
+      }
+    }
+    if (kT) {  // 8 columns s by 32 rows r at a time; columns of rows above are zero
+      __syncthreads();
+      uint32_t* out = reinterpret_cast<uint32_t*>(w.tinvt + (size_t)i * 32 * 128);
+      for (int j = warp; j < 128; j += 8) {
+        const int term = j >> 6, sb = (j >> 2) & 15, rg = j & 3;
+        if (rg < sb >> 2) continue;
+        uint32_t v[4];
+        ldmatrix4_trans(
+            ia + (term * 2 + (sb >> 3)) * kBlk + sw128_offset(rg * 32 + lane, sb & 7), v);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          out[((term * 16 + rg * 4 + m) * 128 + sb * 8 + (lane >> 2)) * 4 + (lane & 3)] = v[m];
+      }
+      __syncthreads();  // the diagonal blocks' place is read
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (kT) {  // 8 columns s by 32 rows r at a time; columns of rows above are zero
-    uint32_t* out = reinterpret_cast<uint32_t*>(w.tinvt + cb * 32 * 128);
-    for (int i = warp; i < 128; i += 8) {
-      const int term = i >> 6, sb = (i >> 2) & 15, rg = i & 3;
-      if (rg < sb >> 2) continue;
-      uint32_t v[4];
-      ldmatrix4_trans(
-          sbase + (term * 2 + (sb >> 3)) * kBlk + sw128_offset(rg * 32 + lane, sb & 7), v);
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        out[((term * 16 + rg * 4 + m) * 128 + sb * 8 + (lane >> 2)) * 4 + (lane & 3)] = v[m];
-    }
-  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -498,11 +536,12 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
 cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
                                   const GdnTcWs& w, cudaStream_t st) {
-  const dim3 grid(w.NC, p.BH);
+  const long items = (long)p.BH * w.NC;
+  const dim3 grid((unsigned)(items < 2 * kGdnSms ? items : 2 * kGdnSms));
   if (w.tinvt)
-    return gdn_launch(&gdn_tc_inverse_kernel<true>, grid, kInvThreads, kISmem, false, st, m.k, p,
+    return gdn_launch(&gdn_tc_inverse_kernel<true>, grid, kInvThreads, inv_smem(true), false, st, m.k, p,
                       x.g, x.beta, w);
-  return gdn_launch(&gdn_tc_inverse_kernel<false>, grid, kInvThreads, kISmem, false, st, m.k, p,
+  return gdn_launch(&gdn_tc_inverse_kernel<false>, grid, kInvThreads, inv_smem(false), false, st, m.k, p,
                     x.g, x.beta, w);
 }
 
