@@ -104,6 +104,15 @@ def test_many_heads(size, init):
     run_case("tc", dict(B=B, NHK=NHK, NH=NH, T=T, DK=DK, DV=DV, init=init), backward=T < 100)
 
 
+@pytest.mark.parametrize("size,backward", [((4, 2, 4, 2437, 64, 64), True),
+                                           ((15, 2, 4, 700, 128, 72), False)], ids=str)
+def test_more_chunks_than_blocks(size, backward):
+    """Every persistent stage takes several items a block (320 and 360 chunks)."""
+    B, NHK, NH, T, DK, DV = size
+    run_case("tc", dict(B=B, NHK=NHK, NH=NH, T=T, DK=DK, DV=DV, gates="reset", seed=4),
+             backward=backward)
+
+
 @pytest.mark.parametrize("gates", ["strong", "hold", "zero_beta", "reset"])
 @pytest.mark.parametrize("keys", ["unit", "alike"])
 def test_many_heads_gates_and_keys(gates, keys):
