@@ -21,6 +21,17 @@ namespace mlstm {
 // context is current or the id cannot be read.
 bool current_context_id(unsigned long long* id);
 
+// Lets a kernel use up to `smem` bytes of dynamic shared memory in the current
+// context.  The limit belongs to the kernel, not to the launch, and host threads
+// share it: `smem` is the most that any launch of the kernel asks for, so that no
+// thread lowers it between another's call here and its launch.  Set once per
+// context and thread (a microsecond a time otherwise).
+cudaError_t allow_smem(const void* kern, size_t smem);
+template <class K>
+cudaError_t allow_smem(K* kern, size_t smem) {
+  return allow_smem(reinterpret_cast<const void*>(kern), smem);
+}
+
 struct DeviceAddressCache {
   static constexpr int kSlots = 16;
   std::mutex mu;

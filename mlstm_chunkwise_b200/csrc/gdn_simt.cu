@@ -10,6 +10,7 @@
 // run chunk after chunk.  1000 tokens x 4 heads of 64 x 96 in fp32: 117 us, 89 of
 // them the recurrence (5.5 us a chunk of two dependent products, bound by their
 // latency: an SM is 9% busy); with z, y and the output on the recurrence it was 206.
+#include "device_address.h"
 #include "gdn.h"
 
 namespace mlstm {
@@ -670,22 +671,17 @@ __global__ void gdn_group_sum(GdnProblem p, const float* __restrict__ dq,
   }
 }
 
-size_t chain_smem(const GdnProblem& p) {
-  return (size_t)(kSa + kSb + 64 * 33 + p.DK * 33 + (p.DK & 1)) * 4 + sizeof(Gates64);
+constexpr size_t chain_smem(int DK) {
+  return (size_t)(kSa + kSb + 64 * 33 + DK * 33 + (DK & 1)) * 4 + sizeof(Gates64);
 }
 constexpr size_t kPrepSmem = (kSa + kSb + 64 * 66 + 64 * 3) * 4;
 constexpr size_t kChunkSmem = (kSa + kSb + 64 * 66) * 4 + sizeof(Gates64);
 constexpr size_t kOutSmem = (kSa + kSb) * 4 + sizeof(Gates64);
 constexpr size_t kGradSmem = (kSa + kSb + 2 * 64 * 65 + 5 * 64 + 64 * 17 + 64 + 128) * 4;
 
-template <class F>
-cudaError_t allow(F* f, size_t smem) {
-  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
-
 template <typename T>
 cudaError_t prep(const GdnProblem& p, const GdnInputs& x, const Ws& w, cudaStream_t st) {
-  cudaError_t e = allow(gdn_simt_prep<T>, kPrepSmem);
+  cudaError_t e = allow_smem(gdn_simt_prep<T>, kPrepSmem);
   if (e != cudaSuccess) return e;
   gdn_simt_prep<T><<<dim3(chunks_of(p.T), p.BH), kThreads, kPrepSmem, st>>>(
       p, (const T*)x.Q, (const T*)x.K, x.g, x.beta, w);
@@ -699,9 +695,9 @@ template <typename T, bool kRev>
 cudaError_t chain(const GdnProblem& p, const GdnInputs& x, const float* init, float* fin, T* dV,
                   const Ws& w, cudaStream_t st) {
   auto go = [&](auto* kern, int cols) {
-    const cudaError_t e = allow(kern, chain_smem(p));
+    const cudaError_t e = allow_smem(kern, chain_smem(1024));  // the widest key's
     if (e != cudaSuccess) return e;
-    kern<<<dim3((p.DV + cols - 1) / cols, p.BH), kThreads, chain_smem(p), st>>>(
+    kern<<<dim3((p.DV + cols - 1) / cols, p.BH), kThreads, chain_smem(p.DK), st>>>(
         p, (const T*)x.K, x.beta, init, fin, dV, w);
     return cudaGetLastError();
   };
@@ -715,7 +711,7 @@ cudaError_t states(const GdnProblem& p, const GdnInputs& x, const void* dH, floa
                    cudaStream_t st) {
   cudaError_t e = prep<T>(p, x, w, st);
   if (e != cudaSuccess) return e;
-  if ((e = allow(gdn_simt_chunk<T, kBw>, kChunkSmem)) != cudaSuccess) return e;
+  if ((e = allow_smem(gdn_simt_chunk<T, kBw>, kChunkSmem)) != cudaSuccess) return e;
   gdn_simt_chunk<T, kBw><<<dim3(chunks_of(p.T), p.BH), kThreads, kChunkSmem, st>>>(
       p, (const T*)x.Q, (const T*)x.K, (const T*)x.V, x.beta, (const T*)dH, w);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -728,7 +724,7 @@ cudaError_t fw(const GdnProblem& p, const GdnInputs& x, void* H, float* C_T, voi
   const Ws w = layout(p, false, static_cast<char*>(ws));
   cudaError_t e = states<T, false>(p, x, nullptr, C_T, w, st);
   if (e != cudaSuccess) return e;
-  if ((e = allow(gdn_simt_out<T>, kOutSmem)) != cudaSuccess) return e;
+  if ((e = allow_smem(gdn_simt_out<T>, kOutSmem)) != cudaSuccess) return e;
   gdn_simt_out<T><<<dim3(chunks_of(p.T), (p.DV + 63) / 64, p.BH), kThreads, kOutSmem, st>>>(
       p, (const T*)x.Q, x.beta, (T*)H, w);
   return cudaGetLastError();
@@ -742,7 +738,7 @@ cudaError_t bw(const GdnProblem& p, const GdnInputs& x, const GdnGrads& d, void*
   cudaError_t e = states<T, true>(p, x, d.dH, nullptr, w, st);
   if (e != cudaSuccess) return e;
   if ((e = chain<T, true>(p, x, d.dC_T, d.dC0, (T*)d.dV, w, st)) != cudaSuccess) return e;
-  if ((e = allow(gdn_simt_grads<T>, kGradSmem)) != cudaSuccess) return e;
+  if ((e = allow_smem(gdn_simt_grads<T>, kGradSmem)) != cudaSuccess) return e;
   gdn_simt_grads<T><<<chunks, kThreads, kGradSmem, st>>>(p, (const T*)x.Q, (const T*)x.K, x.beta,
                                                          (const T*)d.dH, (T*)d.dQ, (T*)d.dK, d.dg,
                                                          d.dbeta, w);

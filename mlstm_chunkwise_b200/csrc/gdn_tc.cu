@@ -363,25 +363,6 @@ bool gdn_tc_supported(const GdnProblem& p) {
   return p.DK <= 128 && p.DK % 8 == 0 && p.DV % 8 == 0;
 }
 
-cudaError_t gdn_allow_smem(const void* kern, size_t smem) {
-  struct Seen {
-    const void* kern;
-    unsigned long long ctx;
-  };
-  static thread_local Seen seen[16] = {};  // more than there are kernels
-  unsigned long long id = 0;
-  const bool known = current_context_id(&id);
-  Seen* free_slot = nullptr;
-  for (Seen& s : seen) {
-    if (known && s.kern == kern && s.ctx == id) return cudaSuccess;
-    if (!free_slot && (!s.kern || s.kern == kern)) free_slot = &s;
-  }
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && known && free_slot) *free_slot = Seen{kern, id};
-  return e;
-}
-
 size_t gdn_tc_workspace(const GdnProblem& p, bool backward) {
   GdnTcWs w{};
   return p.T > 0 ? carve(p, backward ? kBwParts : fw_parts(p), nullptr, &w) : 0;

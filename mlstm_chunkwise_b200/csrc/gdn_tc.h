@@ -98,10 +98,6 @@ struct GdnMaps {
   CUtensorMap q, k, v, h, dh, dv, dq, dk;
 };
 
-// Lets a kernel use `smem` bytes in the current context (set once per context and
-// thread, a microsecond a time otherwise).
-cudaError_t gdn_allow_smem(const void* kern, size_t smem);
-
 // Launches a stage.  `after`: it may start while the stage before it in the
 // stream still runs (programmatic launch): its prologue and its loads of the
 // caller's arrays then overlap that stage's end, and gdn_wait_stage() below
@@ -109,7 +105,7 @@ cudaError_t gdn_allow_smem(const void* kern, size_t smem);
 template <class K, class... A>
 cudaError_t gdn_launch(K* kern, dim3 grid, int threads, size_t smem, bool after, cudaStream_t st,
                        const A&... args) {
-  const cudaError_t e = gdn_allow_smem(reinterpret_cast<const void*>(kern), smem);
+  const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;

@@ -16,6 +16,7 @@
 // from call to call).
 #include <type_traits>
 
+#include "device_address.h"
 #include "head_norm.h"
 
 namespace mlstm {
@@ -419,6 +420,14 @@ int blocks_per_head(const HeadNormProblem& p, const Shape& s, int per_sm, int le
 // partial sums, hence four rows each at least.
 int bw_blocks(const HeadNormProblem& p, const Shape& s) { return blocks_per_head(p, s, 2, 4); }
 
+// The largest ring of `slots` 16-byte vectors a thread, whatever this launch's is: 512
+// threads where a block takes a row, 256 where a warp does.
+template <class K>
+cudaError_t allow_ring(K* kern, int slots, bool block_row) {
+  const size_t most = (size_t)slots * 16 * (block_row ? 512 : 256);
+  return most > 47 * 1024 ? allow_smem(kern, most) : cudaSuccess;  // 1 KB is static
+}
+
 template <typename T, int kVec, int kNV>
 cudaError_t fw(const HeadNormProblem& p, const Shape& s, const void* X, const float* weight,
                const float* bias, void* Y, float* mean, float* rstd, cudaStream_t st) {
@@ -426,11 +435,8 @@ cudaError_t fw(const HeadNormProblem& p, const Shape& s, const void* X, const fl
   const size_t smem = kVec > 1 ? (size_t)kStages * kNV * 16 * s.threads : 0;
   auto kern = s.block_row ? head_norm_fw_kernel<T, kVec, kNV, true>
                           : head_norm_fw_kernel<T, kVec, kNV, false>;
-  if (smem > 47 * 1024) {  // the static part is in the 48 KB, too
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_ring(kern, kVec > 1 ? kStages * kNV : 0, s.block_row);
+  if (e != cudaSuccess) return e;
   kern<<<grid, s.threads, smem, st>>>(p, (const T*)X, weight, bias, (T*)Y, mean, rstd);
   return cudaGetLastError();
 }
@@ -446,9 +452,7 @@ cudaError_t bw(const HeadNormProblem& p, const Shape& s, const void* X, const vo
   const size_t smem = sums > ring ? sums : ring;
   auto kern = s.block_row ? head_norm_bw_kernel<T, kVec, kNV, true>
                           : head_norm_bw_kernel<T, kVec, kNV, false>;
-  cudaError_t e = cudaSuccess;
-  if (smem > 47 * 1024)  // the static part is in the 48 KB, too
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_ring(kern, kVec > 1 ? 2 * kBwStages<kNV> * kNV : 0, s.block_row);
   if (e != cudaSuccess) return e;
   kern<<<grid, s.threads, smem, st>>>(p, (const T*)X, (const T*)dY, weight, mean, rstd, (T*)dX,
                                       part, dbias != nullptr);

@@ -90,6 +90,26 @@ bool current_context_id(unsigned long long* id) {
   return g_ctx_id(ctx, id) == CUDA_SUCCESS;
 }
 
+cudaError_t allow_smem(const void* kern, size_t smem) {
+  struct Seen {
+    const void* kern;
+    unsigned long long ctx;
+  };
+  static thread_local Seen seen[64] = {};  // more than there are kernels
+  unsigned long long id = 0;
+  const bool known = current_context_id(&id);
+  Seen* free_slot = nullptr;
+  for (Seen& s : seen) {
+    if (known && s.kern == kern && s.ctx == id) return cudaSuccess;
+    if (!free_slot && (!s.kern || s.kern == kern)) free_slot = &s;
+    if (!s.kern) break;  // slots are taken in order
+  }
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && known && free_slot) *free_slot = Seen{kern, id};
+  return e;
+}
+
 bool encode_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t d0, uint64_t d1,
                     uint64_t d2, uint32_t b0, uint32_t b1, int swizzle_bytes) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
