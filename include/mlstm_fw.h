@@ -279,8 +279,8 @@ mlstm_status mlstm_step(const void* q, const void* k, const void* v, const float
  *   and value head n reads head n / (NH / NHK) of Q and K;
  *   g, beta [B, NH, T] fp32: g <= 0 (values below -1000, -inf among them, act
  *   as -1000: the state is forgotten entirely, which starts a new sequence
- *   inside a row); beta = 0 writes nothing, so g = beta = 0 on padded tokens
- *   leaves the state as it was;
+ *   inside a row; a NaN stays one); beta = 0 writes nothing, so g = beta = 0 on
+ *   padded tokens leaves the state as it was;
  *   C0 (nullable: zero), C_T (nullable) [B, NH, DK, DV] fp32.
  * Contiguous; 16-byte aligned but for g, beta and their gradients (4 bytes).
  * Sizes: B, NHK, NH >= 1, T >= 0 (up to 2^22), DK, DV in [1, 1024], B * NH up

@@ -50,8 +50,12 @@ __host__ __device__ __forceinline__ int gdn_key_head(const GdnProblem& p, int bh
 }
 
 // g below this decays any state to zero in fp32; clamping it (and -inf) keeps
-// differences of sums finite.
+// differences of sums finite.  A comparison, not fmaxf(), which drops a NaN: a
+// diverged gate must not pass for a reset.
 constexpr float kGdnMinLogDecay = -1000.f;
+__device__ __forceinline__ float gdn_log_decay(float g) {
+  return g < kGdnMinLogDecay ? kGdnMinLogDecay : g;
+}
 
 struct GdnInputs {
   const void *Q, *K, *V;

@@ -152,8 +152,8 @@ gdn_simt_prep(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
   const T* Qp = Q + (kh * p.T + t0) * p.DK;
   const long gt = (long)bh * p.T + t0;
   if (tid < 32) {  // inclusive sums in 64 bits, two tokens per lane
-    double a = 2 * tid < n ? (double)fmaxf(g[gt + 2 * tid], kGdnMinLogDecay) : 0.;
-    double b = 2 * tid + 1 < n ? (double)fmaxf(g[gt + 2 * tid + 1], kGdnMinLogDecay) : 0.;
+    double a = 2 * tid < n ? (double)gdn_log_decay(g[gt + 2 * tid]) : 0.;
+    double b = 2 * tid + 1 < n ? (double)gdn_log_decay(g[gt + 2 * tid + 1]) : 0.;
     double s = a + b;
     for (int o = 1; o < 32; o <<= 1) {
       const double u = __shfl_up_sync(0xffffffffu, s, o);

@@ -83,7 +83,7 @@ gdn_step_kernel(GdnProblem p, const T* __restrict__ q, const T* __restrict__ k,
     const int r = ty + i * kTY;
     c[i] = r < p.DK ? load4<kVec>(cp + (long)r * p.DV, left) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const float a = expf(fmaxf(g[bh], kGdnMinLogDecay)), b = beta[bh];
+  const float a = expf(gdn_log_decay(g[bh])), b = beta[bh];
   float kq = 0.f;
   for (int i = threadIdx.x; i < p.DK; i += kThreads) {
     const float kk = to_float(k[kh * p.DK + i]), qq = to_float(q[kh * p.DK + i]);

@@ -440,7 +440,7 @@ __device__ __forceinline__ void gdn_chunk_sums(const float* g, int n, int lane, 
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int t = 4 * lane + e;
-    s += t < n ? (double)fmaxf(g[t], kGdnMinLogDecay) : 0.;
+    s += t < n ? (double)gdn_log_decay(g[t]) : 0.;
     x[e] = s;
   }
   double incl = s;

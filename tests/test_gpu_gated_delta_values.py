@@ -1,0 +1,53 @@
+"""Gated delta rule on the GPU: values that are not finite, and how exact the
+decays and the fp32 outputs are."""
+import pytest
+import torch
+
+import gated_delta_cases as gd
+from mlstm_chunkwise_b200 import _lib, api
+
+pytestmark = pytest.mark.gpu
+
+# (algorithm, batch, heads, tokens, the token's chunk length): the fp32 path, the
+# staged tensor-core forward, and the fused one (many heads; one chunk)
+PATHS = [("simt", 1, 2, 300, 64), ("tc", 1, 2, 700, 128), ("tc", 40, 4, 300, 128),
+         ("tc", 2, 2, 100, 128)]
+
+
+@pytest.mark.parametrize("algo,B,NH,T,L", PATHS, ids=str)
+def test_nan_gate_is_no_reset(algo, B, NH, T, L):
+    """A NaN in one head's g: that head's outputs from the token on and its final
+    state are NaN, gradients too; chunks before and other heads keep their bits."""
+    x = gd.cuda(gd.make(B=B, NHK=NH, NH=NH, T=T, DK=64, DV=72))
+    dH = torch.randn_like(x["V"])
+
+    def both():
+        H, C = api.gated_delta_fw(*(x[n] for n in gd.NAMES), algo=algo)
+        return H, C, api.gated_delta_bw(*(x[n] for n in gd.NAMES[:5]), dH, x["C0"], algo=algo)
+
+    H, C, d = both()
+    t = T - T // 4
+    x["g"][0, 1, t] = float("nan")
+    H2, C2, d2 = both()
+    torch.cuda.synchronize()
+    assert api.last_device_error() == _lib.OK
+    assert H2[0, 1, t:].isnan().all() and C2[0, 1].isnan().all()
+    assert torch.equal(H2[0, 1, :t // L * L], H[0, 1, :t // L * L])
+    for n in ("dg", "dbeta", "dQ", "dK"):
+        assert d2[n][0, 1, t].isnan().all(), n
+    others = torch.ones(B, NH, dtype=torch.bool)
+    others[0, 1] = False
+    for a, b in ((H, H2), (C, C2), *((d[n], d2[n]) for n in d)):
+        assert torch.equal(a[others], b[others])
+
+
+@pytest.mark.parametrize("DV", [64, 7])
+def test_nan_gate_in_a_step(DV):
+    x = gd.cuda(gd.make(NHK=2, NH=2, T=1, DK=64, DV=DV))
+    tok = [x[n][:, :, 0].contiguous() for n in gd.NAMES[:5]]
+    C, C2 = x["C0"].clone(), x["C0"].clone()
+    h = api.gated_delta_step(*tok, C)
+    tok[3][0, 1] = float("nan")
+    h2 = api.gated_delta_step(*tok, C2)
+    assert C2[0, 1].isnan().all() and h2[0, 1].isnan().all()
+    assert torch.equal(C[0, 0], C2[0, 0]) and torch.equal(h[0, 0], h2[0, 0])
