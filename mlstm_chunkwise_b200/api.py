@@ -49,6 +49,12 @@ def _check_tensor(name, t, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _written(*tensors):
+    """Raises the versions of the caller's tensors that a call wrote in place:
+    autograd then refuses a backward that kept them from before."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def workspace_size(B, NH, T, DK, DV, chunk_size, dtype=torch.bfloat16, algo="auto") -> int:
     n = ctypes.c_size_t(0)
     _lib.check(_lib.lib().mlstm_fw_workspace_size(B, NH, T, DK, DV, chunk_size, _DT[dtype],
@@ -460,7 +466,7 @@ def gated_delta_fw(Q, K, V, g, beta, C0=None, *, scale: float | None = None, alg
     T = Q.shape[2]
     B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(Q, K, V, g, beta, C0, (T,))
     out = {} if out is None else out
-    H, C_T = out.get("H"), out.get("C_T") if return_last_state else None
+    given = H, C_T = out.get("H"), out.get("C_T") if return_last_state else None
     if H is None:
         H = torch.empty_like(V)
     else:
@@ -481,6 +487,8 @@ def gated_delta_fw(Q, K, V, g, beta, C0=None, *, scale: float | None = None, alg
             NH, T, DK, DV, DK ** -0.5 if scale is None else float(scale), _DT[dt], _ALGO[algo],
             _ptr(workspace), workspace.numel(), _stream(dev))
     _lib.check(st, "mlstm_gated_delta_fw")
+    if out:
+        _written(*given)
     return (H, C_T) if return_last_state else H
 
 
@@ -595,6 +603,7 @@ def gated_delta_step(q, k, v, g, beta, C, *, scale: float | None = None, h=None)
     float32 (overwritten).  Returns h [B,NH,DV] in the input dtype (``h`` may be
     given)."""
     B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(q, k, v, g, beta, C, ())
+    given = h
     if h is None:
         h = torch.empty_like(v)
     else:
@@ -604,6 +613,7 @@ def gated_delta_step(q, k, v, g, beta, C, *, scale: float | None = None, h=None)
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(C), _ptr(h), B, NHK, NH, DK, DV,
             DK ** -0.5 if scale is None else float(scale), _DT[dt], _stream(dev))
     _lib.check(st, "mlstm_gated_delta_step")
+    _written(C, given)
     return h
 
 
@@ -685,6 +695,8 @@ def head_norm_fw(X, weight, bias=None, *, eps: float = 1e-5, out: torch.Tensor |
                                            _ptr(rstd), B, NH, T, D, float(eps), _DT[dt],
                                            _stream(dev))
     _lib.check(st, "mlstm_head_norm_fw")
+    if out is not None:
+        _written(out)
     return Y, mean, rstd
 
 

@@ -51,3 +51,43 @@ def test_nan_gate_in_a_step(DV):
     h2 = api.gated_delta_step(*tok, C2)
     assert C2[0, 1].isnan().all() and h2[0, 1].isnan().all()
     assert torch.equal(C[0, 0], C2[0, 0]) and torch.equal(h[0, 0], h2[0, 0])
+
+
+def kept(**kw):
+    """Leaves, the output of a call that keeps its inputs, and its initial state
+    as a tensor of the caller's own."""
+    d = {n: v.requires_grad_() for n, v in gd.cuda(gd.make(T=80, **kw)).items()}
+    state = d["C0"].detach()
+    H, _ = api.gated_delta_chunkwise(*(d[n] for n in gd.NAMES), recompute=True)
+    return d, state, H
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_autograd_sees_writes_in_place(dtype):
+    """A state that a later call overwrites is not used for gradients."""
+    modified = pytest.raises(RuntimeError, match="modified by an inplace operation")
+    d, state, H = kept(dtype=dtype)
+    tok = [d[n].detach()[:, :, 0].contiguous() for n in gd.NAMES[:5]]
+    api.gated_delta_step(*tok, state)
+    with modified:
+        H.float().sum().backward()
+    d, state, H = kept(dtype=dtype)
+    api.gated_delta_fw(*(d[n].detach() for n in gd.NAMES), out={"C_T": state})
+    with modified:
+        H.float().sum().backward()
+    d, state, H = kept(dtype=dtype)
+    api.gated_delta_fw(*(d[n].detach() for n in gd.NAMES), out={"H": d["V"].detach().clone()})
+    H.float().sum().backward()  # nothing that was kept
+
+
+def test_outputs_given_by_the_caller_are_marked():
+    x = gd.cuda(gd.make(T=80))
+    H, h = torch.empty_like(x["V"]), torch.empty_like(x["V"][:, :, 0])
+    Y = torch.empty(1, 80, 2 * 64, dtype=torch.bfloat16, device="cuda")
+    api.gated_delta_fw(*(x[n] for n in gd.NAMES), out={"H": H}, return_last_state=False)
+    api.gated_delta_step(*(x[n][:, :, 0].contiguous() for n in gd.NAMES[:5]), x["C0"], h=h)
+    api.head_norm_fw(H, torch.ones(2, 64, device="cuda"), out=Y)
+    assert [t._version for t in (H, h, x["C0"], Y)] == [1, 1, 1, 1]
+    with torch.inference_mode():
+        C = x["C0"].clone()  # tensors without a version
+        api.gated_delta_step(*(x[n][:, :, 0].contiguous() for n in gd.NAMES[:5]), C)
