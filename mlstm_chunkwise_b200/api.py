@@ -141,6 +141,8 @@ def mlstm_fw(Q, K, V, i_pre, f_pre, C0=None, n0=None, m0=None, *, chunk_size: in
         _ptr(H), _ptr(C_T), _ptr(n_T), _ptr(m_T), B, NH, T, DK, DV, chunk_size, _DT[dt],
         _GATE[gate_mode], _ALGO[algo], _ptr(workspace), workspace.numel(), _stream(dev))
     _lib.check(st, "mlstm_fw")
+    if out:
+        _written(out.get("H"), *(out.get(n) for n in ("C_T", "n_T", "m_T") if return_last_states))
     if return_last_states:
         return H, (C_T, n_T, m_T)
     return H
@@ -262,6 +264,7 @@ def mlstm_step(q, k, v, i_pre, f_pre, C, n, m, *, gate_mode: str = "exp", h=None
     _check_tensor("n", n, torch.float32, (B, NH, DK), dev)
     for name, t in (("q", q), ("k", k), ("v", v)):
         _check_tensor(name, t, dt, tuple(t.shape), dev)
+    given = h
     if h is None:
         h = torch.empty((B, NH, DV), dtype=dt, device=dev)
     _check_tensor("h", h, dt, (B, NH, DV), dev)
@@ -269,6 +272,7 @@ def mlstm_step(q, k, v, i_pre, f_pre, C, n, m, *, gate_mode: str = "exp", h=None
                                _ptr(n), _ptr(m), _ptr(h), B, NH, DK, DV, _DT[dt],
                                _GATE[gate_mode], _stream(dev))
     _lib.check(st, "mlstm_step")
+    _written(C, n, m, given)
     return h
 
 
