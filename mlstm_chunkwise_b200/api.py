@@ -625,8 +625,8 @@ class _GatedDelta(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, g, beta, C0, scale, algo, recompute):
         saved = None
-        if not recompute and algo == "auto" and any(ctx.needs_input_grad) and Q.dim() == 4 and \
-                V.dim() == 4 and Q.dtype in _DT and \
+        if not recompute and algo == "auto" and Q.dim() == 4 and V.dim() == 4 and \
+                Q.dtype in _DT and \
                 gated_delta_train_sizes(Q.shape[0], Q.shape[1], V.shape[1], Q.shape[2],
                                         Q.shape[3], V.shape[3], Q.dtype) is not None:
             H, C_T, saved = gated_delta_fw_train(Q, K, V, g, beta, C0, scale=scale)
@@ -659,10 +659,16 @@ def gated_delta_chunkwise(Q, K, V, g, beta, C0=None, *, scale: float | None = No
     gradients of losses on H and on C_T reach Q, K, V, g, beta and C0.  Where
     the training pair exists (``gated_delta_train_sizes``) the forward keeps
     about 2.1 KB per token and head (DK = DV = 128) for the backward;
-    ``recompute=True`` keeps the inputs alone and recomputes the forward.
+    ``recompute=True`` keeps the inputs alone and recomputes the forward.  Where
+    nothing will be differentiated (``torch.no_grad()``, no input that requires a
+    gradient) it is ``gated_delta_fw``.
     (Capture of a backward pass into a CUDA graph: as with any autograd
     function, not while an eager graph holds the same leaves; differentiate
     ``x.detach()``.)"""
+    # asked here: inside the function an input's requires_grad says nothing of no_grad()
+    if not torch.is_grad_enabled() or \
+            not any(t is not None and t.requires_grad for t in (Q, K, V, g, beta, C0)):
+        return gated_delta_fw(Q, K, V, g, beta, C0, scale=scale, algo=algo)
     return _GatedDelta.apply(Q, K, V, g, beta, C0, scale, algo, recompute)
 
 

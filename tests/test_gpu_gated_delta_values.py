@@ -91,3 +91,25 @@ def test_outputs_given_by_the_caller_are_marked():
     with torch.inference_mode():
         C = x["C0"].clone()  # tensors without a version
         api.gated_delta_step(*(x[n][:, :, 0].contiguous() for n in gd.NAMES[:5]), C)
+
+
+def test_no_training_forward_where_nothing_is_differentiated():
+    """Under no_grad, with a state that requires a gradient (and with no such
+    input), the call is gated_delta_fw: its bits and its launches."""
+    x = gd.cuda(gd.make(B=40, NHK=4, NH=4, T=300))
+    launches = _lib.lib().mlstm_kernel_launches
+
+    def count(call):
+        n = launches()
+        return call(), launches() - n
+
+    want, n = count(lambda: api.gated_delta_fw(*(x[m] for m in gd.NAMES)))
+    plain = count(lambda: api.gated_delta_chunkwise(*(x[m] for m in gd.NAMES)))
+    x["C0"].requires_grad_()
+    with torch.no_grad():
+        off = count(lambda: api.gated_delta_chunkwise(*(x[m] for m in gd.NAMES)))
+    for got, k in (plain, off):
+        assert k == n and all(torch.equal(a, b) for a, b in zip(got, want))
+        assert not any(t.requires_grad for t in got)
+    got, k = count(lambda: api.gated_delta_chunkwise(*(x[m] for m in gd.NAMES)))
+    assert k > n and all(t.requires_grad for t in got)
