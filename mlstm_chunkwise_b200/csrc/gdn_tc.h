@@ -226,9 +226,19 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-// e^{a - b} of two sums of g held as (hi, lo).
+constexpr float kLog2eLo = (float)(1.4426950408889634 - (double)kLog2e);
+// e^{a - b} of two sums of g held as (hi, lo), off by no more than ex2.approx itself
+// (2^-22 of the value): what the difference and the exponent lose in fp32, which
+// grows with their size, is carried along and put right to first order.  Without
+// that, factors e^{-x} and e^{x} whose product is of order one left 2.4e-6 of it
+// at x = 15 and 8e-6 at 56.
 __device__ __forceinline__ float gdn_decay(float2 a, float2 b) {
-  return ex2_approx(((a.x - b.x) + (a.y - b.y)) * kLog2e);
+  const float d = a.x - b.x, v = d - a.x;
+  const float dl = ((a.x - (d - v)) - (b.x + v)) + (a.y - b.y);
+  const float t = d * kLog2e;
+  const float tl = fmaf(d, kLog2e, -t) + fmaf(d, kLog2eLo, dl * kLog2e);
+  const float e = ex2_approx(t);
+  return fmaf(e, tl * 0.6931471805599453f, e);
 }
 __device__ __forceinline__ float gdn_exp(float2 a) { return expf(a.x + a.y); }
 
@@ -250,8 +260,8 @@ __device__ __forceinline__ bool elect_one() {
 // below one, e^{gc_r - gc_m} e^{gc_m - gc_s} with m the block's last token (or,
 // transposed, e^{gc_t - gc_m} e^{gc_m - gc_r} with m its first), so that one
 // exponential per row and one per column replace one per element.
-// In the diagonal's block the two would be above and below one: exact as long as
-// the block's whole decay stays within fp32 (kGdnFlat), else one by one.
+// In the diagonal's block the two are above and below one: as accurate there, as
+// long as the block's whole decay stays within fp32 (kGdnFlat), else one by one.
 constexpr float kGdnFlat = 60.f;
 // Factor of column s, by the thread of token s (a warp holds a block).
 __device__ __forceinline__ float gdn_col_factor(float2 g, int m) {

@@ -113,3 +113,29 @@ def test_no_training_forward_where_nothing_is_differentiated():
         assert not any(t.requires_grad for t in got)
     got, k = count(lambda: api.gated_delta_chunkwise(*(x[m] for m in gd.NAMES)))
     assert k > n and all(t.requires_grad for t in got)
+
+
+@pytest.mark.parametrize("decay", [2.0, 15.0, 31.0, 44.0, 56.0, 75.0])
+def test_decays_of_neighbours(decay):
+    """e^{g_{s+1}} as dbeta_s alone shows it: keys are the unit vectors, so that y
+    is V, and each query is the key before, so that
+        dbeta_s = e^{g_{s+1}} dH_{s+1}.v_s
+    with an exact integer behind the decay.  `decay` is that of 32 tokens: up to 60
+    Gam is the product of two factors, of which the larger is e^decay.  Two
+    exponentials and a quotient, each off by 2^-22, and eight roundings of 2^-24:
+    3 x 2^-22 + 8 x 2^-24 = 1.2e-6."""
+    T = DK = 128
+    gen = torch.Generator().manual_seed(int(decay))
+    g = -decay / 32 * (0.5 + torch.rand(1, 1, T, generator=gen))
+    g = g * (decay / 32) / -g.mean()
+    eye = torch.eye(T).view(1, 1, T, DK)
+    V, dH = (torch.randint(-4, 5, (1, 1, T, 64), generator=gen).float() for _ in range(2))
+    x = {"Q": eye.roll(1, 2), "K": eye, "V": V, "g": g, "beta": torch.rand(1, 1, T, generator=gen)}
+    d = {n: (v if n in ("g", "beta") else v.bfloat16()).contiguous().cuda() for n, v in x.items()}
+    got = api.gated_delta_bw(*d.values(), dH.bfloat16().cuda(), scale=1.0, algo="tc")["dbeta"]
+    dots = (dH[:, :, 1:] * V[:, :, :-1]).sum(-1).double()
+    want = torch.exp(g[:, :, 1:].double()) * dots
+    err = (got[0, 0, :-1].double().cpu() - want[0, 0]).abs() / want[0, 0].abs().clamp(min=1e-300)
+    # token 0's query is the last token's key, which it does not see
+    assert float(err[dots[0, 0] != 0].max()) < 1.2e-6
+    assert not got[0, 0, :-1].cpu()[dots[0, 0] == 0].any() and got[0, 0, -1] == 0
