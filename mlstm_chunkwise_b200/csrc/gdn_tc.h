@@ -189,10 +189,11 @@ __device__ __forceinline__ void split_pack(const float* x, uint32_t (&hi)[N / 2]
   }
 }
 // Eight values as 16-byte piece c of row r of a block in kTerms terms, `term`
-// bytes apart; kFrom: the first term that is written.
+// bytes apart, but for the third where `third` says how far it lies from the first;
+// kFrom: the first term that is written.
 template <int kTerms, int kFrom = 0>
 __device__ __forceinline__ void put_terms(uint8_t* img, uint32_t term, int r, int c,
-                                          const float* x) {
+                                          const float* x, int third = 0) {
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = x[e];
@@ -204,8 +205,8 @@ __device__ __forceinline__ void put_terms(uint8_t* img, uint32_t term, int r, in
       v[e] = t + 1 < kTerms ? take_pair(y[2 * e], y[2 * e + 1])
                             : pack_bf16x2(y[2 * e], y[2 * e + 1]);
     if (t >= kFrom)
-      *reinterpret_cast<uint4*>(img + (t - kFrom) * term + sw128_offset(r, c)) =
-          make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4*>(img + (t == 2 && third ? third : (int)((t - kFrom) * term)) +
+                                sw128_offset(r, c)) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 __device__ __forceinline__ void put8(uint8_t* img, uint32_t term, int r, int c, const float* x) {

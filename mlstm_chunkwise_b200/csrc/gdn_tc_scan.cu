@@ -6,16 +6,18 @@
 //   X = K S               under H's pass of the chunk before
 //   Q S                   under z's pass (z = V - Lam X)
 //   y = Tinv z            meanwhile Q S is scaled in place
-//                         the image of D beta y
+//                         the image of D beta y in three terms, the third in V's place
 //   Q K^T, S = e^G S + K^T (D beta y)   meanwhile the image of y, then P
 //   H = scale (Lam Q S + P y)           meanwhile the next state's image, e^G S
-// 104 products of 128 x 128 x 16 (7300 cycles), behind each of which a barrier of its
-// own lets the rows go on: 8 to 8.5 us a chunk, against 10.5 when each of four rounds
-// waited for all of its products.  Behind the staged forward where few heads with
-// many chunks leave SMs idle, see gdn_tc_fw_fused().
+// 112 products of 128 x 128 x 16 (7900 cycles), behind each of which a barrier of its
+// own lets the rows go on: 8.5 to 9 us a chunk (half a us of it the third term, without
+// which the final state of one chunk was off by 3.4e-6 in place of 1.5e-6), against
+// 10.5 when each of four rounds waited for all of its products.  Asking L2 for the
+// next chunk's tiles ahead changed nothing.  Behind the staged forward where few
+// heads with many chunks leave SMs idle, see gdn_tc_fw_fused().
 // Tensor memory: S [0, 128), X and y [128, 256), Tinv then Q K^T and P [256, 384),
-// Q S then H [384, 512).  Shared memory blocks: K 0, 1; Q 2, 3; V 4, 5; z, y, H 6..9;
-// D beta y, then the state's image 10..13.
+// Q S then H [384, 512).  Shared memory blocks: K 0, 1; Q 2, 3; V, then D beta y's third
+// term 4, 5; z, y, H 6..9; D beta y, then the state's image 10..13.
 #include <cuda.h>
 
 #include "gdn_tc.h"
@@ -173,22 +175,23 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
         mma_commit(bar_y);
       }
       __syncwarp();
-      if (lead && more) load_v(c + 1);
-      __syncwarp();
       sync();  // D beta y
       if (elect_one()) {
         if (ok)
           mma_ss<false, false>(tmem + 256, qa, ka, idesc_bf16(128, 128, 0, 0), slabs, true);
         mma_commit(bar_p);
         if (ok)
-          for (int t = 0; t < 2; ++t)
-            mma_ss<true, true>(tmem, ka, ua + 2 * t * kBlk, idt, 2, false);
+          for (int t = 0; t < 3; ++t)
+            mma_ss<true, true>(tmem, ka, t < 2 ? ua + 2 * t * kBlk : va, idt, 2, false);
         mma_commit(bar_s);
       }
       __syncwarp();
       if (lead && more) {
         wait(bar_s, ph, 0x82);
-        if (ok) load_qk(c + 1);
+        if (ok) {
+          load_qk(c + 1);
+          load_v(c + 1);
+        }
       }
       __syncwarp();
       sync();  // P, y
@@ -278,7 +281,7 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = dec * __uint_as_float(v[8 * cc + e]);
-          put8(imgu, 2 * kBlk, r, (h & 1) * 4 + cc, y);
+          put_terms<3>(imgu, 2 * kBlk, r, (h & 1) * 4 + cc, y, (int)kOffV - (int)kOffU);
         }
       }
       sync();
@@ -358,16 +361,18 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 }  // namespace
 
-// By what the two cost in us, measured: a chunk takes a fused block 8.5; the staged
+// By what the two cost in us, measured: a chunk takes a fused block 9; the staged
 // forward takes a wave of 148 (head, chunk, pair of value tiles) 21 (mn and out),
 // its recurrence 1.45 a chunk, and two more launches 5.  So the fused one runs for
-// one or two chunks, and from about a quarter of a wave of heads on.  (64 chunks,
-// 128 x 128, us staged and fused: 16 heads 293, 520; 48 heads 597, 583; 256 heads
-// 3207, 1517.  16 chunks: 32 heads 134, 147; 48 heads 177, 159.)
+// one to three chunks, and from about a third of a wave of heads on.  (64 chunks,
+// 128 x 128, us staged and fused: 32 heads 417, 585; 48 heads 574, 618; 56 heads 660,
+// 635; 64 heads 740, 646.  32 chunks: 148 heads 890, 413; 256 heads 1480, 761.  16
+// chunks: 16 heads 87, 153; 40 heads 157, 167; 48 heads 178, 171.  16 heads: 2 chunks
+// 52, 42; 3 chunks 52, 50.)
 bool gdn_tc_fw_fused(const GdnProblem& p) {
   const long nc = gdn_tc_chunks(p), heads = (long)p.BH * ((p.DV + 127) / 128);
   auto waves = [](long n) { return (n + kGdnSms - 1) / kGdnSms; };
-  const long fused = 850 * nc * waves(heads);
+  const long fused = 900 * nc * waves(heads);
   const long staged = 2100 * waves(heads * nc) +
                       145 * nc * waves((long)p.BH * ((p.DV + 63) / 64)) + 500;
   return fused <= staged;

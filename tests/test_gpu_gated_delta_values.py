@@ -139,3 +139,34 @@ def test_decays_of_neighbours(decay):
     # token 0's query is the last token's key, which it does not see
     assert float(err[dots[0, 0] != 0].max()) < 1.2e-6
     assert not got[0, 0, :-1].cpu()[dots[0, 0] == 0].any() and got[0, 0, -1] == 0
+
+
+@pytest.mark.parametrize("B,T", [(1, 128), (60, 300), (1, 640)], ids=str)
+def test_the_final_state_keeps_24_bits_of_what_is_written(B, T):
+    """With unit vectors as keys y is V, and row t of the final state is
+    D_t beta_t v_t: the decay (2^-22), the last operand of the state's product in
+    three terms (2^-24), and the products and sums around it (twelve of 2^-24):
+    2^-22 + 13 x 2^-24 < 2^-19.  On the fused forward (one chunk; many heads) and the
+    staged one (640 tokens of one head); a reset in front of the last 128 tokens
+    makes them a sequence of their own."""
+    L = DK = 128
+    gen = torch.Generator().manual_seed(3)
+    g = -0.02 * torch.rand(B, 1, T, generator=gen)
+    beta = torch.rand(B, 1, T, generator=gen)
+    t0 = (T - 1) // L * L
+    if t0:
+        g[:, :, t0] = float("-inf")
+    V = torch.randint(-9, 10, (B, 1, T, 72), generator=gen).float()
+    K = torch.eye(L)[torch.arange(T) % L].expand(B, 1, T, DK)
+    x = [t.contiguous().bfloat16().cuda() for t in (K, K, V)]
+    _, C = api.gated_delta_fw(*x, g.cuda(), beta.cuda(), algo="tc")
+    G, n = g[:, :, t0:].double(), T - t0
+    if t0:
+        G[:, :, 0] = 0.0
+    D = torch.exp(G.flip(-1).cumsum(-1).flip(-1) - G)  # the decays behind each token
+    want = (D * beta[:, :, t0:].double())[..., None] * V[:, :, t0:].double()
+    C = C.double().cpu()
+    assert not C[:, :, n:].any()
+    err = (C[:, :, :n] - want).abs() / want.abs().clamp(min=1e-300)
+    assert float(err[want != 0].max()) < 2.0 ** -19
+    assert not C[:, :, :n][want == 0].any()
