@@ -282,6 +282,11 @@ mlstm_status mlstm_step(const void* q, const void* k, const void* v, const float
  *   inside a row; a NaN stays one); beta = 0 writes nothing, so g = beta = 0 on
  *   padded tokens leaves the state as it was;
  *   C0 (nullable: zero), C_T (nullable) [B, NH, DK, DV] fp32.
+ * Values are finite.  A reset at a head's first token forgets C0 whatever it holds;
+ * elsewhere an infinity or a NaN reaches all tokens of its chunk (128 tokens, or 64),
+ * those in front of it too, and what follows, resets and padding included (0 times an
+ * infinity is a NaN), and in the gradients all of its head (and key head).  It does
+ * not reach other heads, nor the outputs of earlier chunks.
  * Contiguous; 16-byte aligned but for g, beta and their gradients (4 bytes).
  * Sizes: B, NHK, NH >= 1, T >= 0 (up to 2^22), DK, DV in [1, 1024], B * NH up
  * to 65535.  T = 0 copies C0 (or zero) to C_T.

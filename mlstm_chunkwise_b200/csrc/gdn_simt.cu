@@ -347,9 +347,13 @@ gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ 
   const int v0 = blockIdx.x * kVT, bh = blockIdx.y, NC = chunks_of(p.T);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const long kh = gdn_key_head(p, bh);
+  // a first token that forgets the state entirely: it may hold anything, and 0 times
+  // an infinity is a NaN
+  const float2 g0 = w.gc[(size_t)bh * NC * kL];
+  const bool have = init && (kRev || expf(g0.x + g0.y) != 0.f);
   for (int i = tid; i < p.DK * kVT; i += kThreads) {
     const int d = i / kVT, v = i % kVT;
-    sS[d * 33 + v] = init && v0 + v < p.DV ? init[((long)bh * p.DK + d) * p.DV + v0 + v] : 0.f;
+    sS[d * 33 + v] = have && v0 + v < p.DV ? init[((long)bh * p.DK + d) * p.DV + v0 + v] : 0.f;
   }
   const float* A = kRev ? w.E : w.W;
   float *Y = kRev ? w.dz : w.y, *St = kRev ? w.dS : w.S;

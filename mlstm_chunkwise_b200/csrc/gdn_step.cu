@@ -114,6 +114,14 @@ gdn_step_kernel(GdnProblem p, const T* __restrict__ q, const T* __restrict__ k,
   kc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < kTY; ++i) fma4(kc, 1.f, red[i * kTX + tx]);
+  // forgotten entirely, whatever it held: 0 times an infinity is a NaN
+  const bool gone = a == 0.f;
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (gone) {
+    kc = none;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) c[i] = none;
+  }
   float4 vn;
   {
     const long vb = (long)bh * p.DV + col;
@@ -130,11 +138,13 @@ gdn_step_kernel(GdnProblem p, const T* __restrict__ q, const T* __restrict__ k,
 #pragma unroll
   for (int i = 0; i < kRows; ++i)
     if (ty + i * kTY < p.DK) put(ty + i * kTY, c[i]);
-  for (int r = ty + kRows * kTY; r < p.DK; r += kTY) put(r, load4<kVec>(cp + (long)r * p.DV, left));
+  for (int r = ty + kRows * kTY; r < p.DK; r += kTY)
+    put(r, gone ? none : load4<kVec>(cp + (long)r * p.DV, left));
   if (ty == 0) {
     qc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kTY; ++i) fma4(qc, 1.f, red[(kTY + i) * kTX + tx]);
+    if (gone) qc = none;
     kq = 0.f;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) kq += dots[i];

@@ -243,6 +243,11 @@ __device__ __forceinline__ float gdn_decay(float2 a, float2 b) {
 }
 __device__ __forceinline__ float gdn_exp(float2 a) { return expf(a.x + a.y); }
 
+// Whether a head's first token forgets the initial state entirely (gc: the sums of its
+// first chunk).  The state is then not read: it may hold anything, and 0 times an
+// infinity is a NaN.
+__device__ __forceinline__ bool gdn_starts_fresh(const float2* gc) { return gdn_exp(gc[0]) == 0.f; }
+
 // True in one lane of a converged warp.  The compiler then knows that a single
 // thread is active and keeps descriptors in uniform registers: a product with A
 // in tensor memory and 64 columns issues in 25 cycles and takes 35, against 44

@@ -128,9 +128,10 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
       gl = w.gc[chunk(i) * kGdnL + kGdnL - 1];
     };
     if (steps > 0) load(0);
+    const bool have = init && r < p.DK && (kRev || !gdn_starts_fresh(w.gc + chunk(0) * kGdnL));
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      s[e] = init && r < p.DK && v0 + e < p.DV ? init[((long)bh * p.DK + r) * p.DV + v0 + e] : 0.f;
+      s[e] = have && v0 + e < p.DV ? init[((long)bh * p.DK + r) * p.DV + v0 + e] : 0.f;
     for (int i = 0; i < NC; ++i) {
       uint8_t* img = smem + kOffS + (i & 1) * kTerms * kBlk;
 #pragma unroll

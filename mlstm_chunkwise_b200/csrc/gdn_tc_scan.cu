@@ -132,9 +132,10 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
   if (cols) {
     uint32_t v[32];
     const float* src = C0 + ((long)bh * p.DK + r) * p.DV + v0;
+    const bool have = C0 && r < p.DK && !gdn_starts_fresh(w.gc + (size_t)bh * NC * kGdnL);
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
-      const bool in = C0 && r < p.DK && v0 + e < p.DV;
+      const bool in = have && v0 + e < p.DV;
       const float4 x = in ? *reinterpret_cast<const float4*>(src + e) : make_float4(0.f, 0.f, 0.f, 0.f);
       v[e] = __float_as_uint(x.x);
       v[e + 1] = __float_as_uint(x.y);

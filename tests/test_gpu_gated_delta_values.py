@@ -170,3 +170,35 @@ def test_the_final_state_keeps_24_bits_of_what_is_written(B, T):
     err = (C[:, :, :n] - want).abs() / want.abs().clamp(min=1e-300)
     assert float(err[want != 0].max()) < 2.0 ** -19
     assert not C[:, :, :n][want == 0].any()
+
+
+@pytest.mark.parametrize("algo,B,NH,T,L", PATHS, ids=str)
+@pytest.mark.parametrize("stale", [float("nan"), float("inf")])
+def test_reset_at_the_first_token_forgets_any_state(algo, B, NH, T, L, stale):
+    """A slot whose last sequence left infinities or NaN: a new sequence that starts
+    with a reset has the bits of one that starts from zeros."""
+    x = gd.cuda(gd.make(B=B, NHK=NH, NH=NH, T=T, DK=64, DV=72))
+    x["g"][0, 1, 0] = float("-inf")
+    dH, dC = torch.randn_like(x["V"]), torch.randn_like(x["C0"])
+
+    def both():
+        d = api.gated_delta_bw(*(x[n] for n in gd.NAMES[:5]), dH, x["C0"], dC, algo=algo)
+        return (*api.gated_delta_fw(*(x[n] for n in gd.NAMES), algo=algo), *d.values())
+
+    x["C0"][0, 1] = 0.0
+    want = both()
+    x["C0"][0, 1] = stale
+    got = both()
+    assert torch.isfinite(got[0]).all() and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("DK,DV", [(64, 64), (33, 7), (256, 40), (1024, 6)])
+def test_reset_in_a_step_forgets_any_state(DK, DV):
+    x = gd.cuda(gd.make(NHK=2, NH=2, T=1, DK=DK, DV=DV))
+    tok = [x[n][:, :, 0].contiguous() for n in gd.NAMES[:5]]
+    tok[3][0, 1] = float("-inf")
+    C = [x["C0"].clone(), x["C0"].clone()]
+    C[0][0, 1], C[1][0, 1] = 0.0, float("nan")
+    C[1][0, 1, ::2] = float("inf")
+    h = [api.gated_delta_step(*tok, c) for c in C]
+    assert torch.isfinite(h[1]).all() and torch.equal(*h) and torch.equal(*C)
