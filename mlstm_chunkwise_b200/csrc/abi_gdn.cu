@@ -88,7 +88,10 @@ mlstm_status norm_problem(int B, int NH, int T, int D, float eps, mlstm_dtype dt
     return MLSTM_ERR_INVALID_ARG;
   if (D > kHeadNormMaxD || T > (1 << 22) || (long long)B * NH > 65535)
     return MLSTM_ERR_UNSUPPORTED;
-  *out = HeadNormProblem{B, NH, T, D, eps};
+  *out = HeadNormProblem{B, NH, T, D, eps, nullptr};
+#ifdef MLSTM_DEBUG_BOUNDS
+  out->err = device_error_word();
+#endif
   return MLSTM_OK;
 }
 
@@ -270,6 +273,9 @@ mlstm_status mlstm_gated_delta_step(const void* q, const void* k, const void* v,
   if (!all_aligned(dtype == MLSTM_DT_BF16 ? 2 : 4, {q, k, v, h}) || !all_aligned(4, {g, beta}) ||
       !all_aligned(16, {C}))
     return MLSTM_ERR_INVALID_ARG;
+#ifdef MLSTM_DEBUG_BOUNDS
+  p.err = device_error_word();
+#endif
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return run_family(MLSTM_KERNEL_GATED_DELTA_STEP, 1, st, [&] {
     return launch_gdn_step(p, dtype, q, k, v, g, beta, C, h, st);

@@ -284,7 +284,8 @@ gdn_simt_chunk(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
     for (int i = 0; i < 4; ++i)
       for (int j = 0; j < 4; ++j) {
         const int r = r0 + ty * 4 + i, cc = c0 + tx * 4 + j;
-        if (r < rows && cc < cols) dst[(long)r * cols + cc] = acc[i][j];
+        if (r < rows && cc < cols && MLSTM_IN_BOUNDS(p, cb < (size_t)p.BH * NC))
+          dst[(long)r * cols + cc] = acc[i][j];
       }
   };
   for (int d0 = 0; d0 < p.DK; d0 += 64) {
@@ -378,7 +379,7 @@ gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ 
       for (int j = 0; j < kTN; ++j) {
         const int r = ty * 4 + i, v = tx * kTN + j;
         const float y = kRev ? add[i][j] + acc[i][j] : add[i][j] - acc[i][j];
-        if (v0 + v < p.DV) {
+        if (v0 + v < p.DV && MLSTM_IN_BOUNDS(p, cb < (size_t)p.BH * NC && r < kL)) {
           Y[(cb * kL + r) * p.DV + v0 + v] = y;
           if (kRev && r < n) dV[((long)bh * p.T + t0 + r) * p.DV + v0 + v] = from_float<T>(y);
         }
@@ -404,7 +405,8 @@ gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ 
           const int d = d0 + ty * 4 + i, v = tx * kTN + j;
           if (d >= p.DK) continue;
           const float old = sS[d * 33 + v];
-          if (v0 + v < p.DV) St[(cb * p.DK + d) * p.DV + v0 + v] = old;
+          if (v0 + v < p.DV && MLSTM_IN_BOUNDS(p, cb < (size_t)p.BH * NC))
+            St[(cb * p.DK + d) * p.DV + v0 + v] = old;
           sS[d * 33 + v] = fmaf(eg, old, kRev ? acc[i][j] + add[i][j] : acc[i][j]);
         }
     }
@@ -413,7 +415,8 @@ gdn_simt_chain(GdnProblem p, const T* __restrict__ K, const float* __restrict__ 
   if (fin)
     for (int i = tid; i < p.DK * kVT; i += kThreads) {
       const int d = i / kVT, v = i % kVT;
-      if (v0 + v < p.DV) fin[((long)bh * p.DK + d) * p.DV + v0 + v] = sS[d * 33 + v];
+      if (v0 + v < p.DV && MLSTM_IN_BOUNDS(p, bh < p.BH && d < p.DK))
+        fin[((long)bh * p.DK + d) * p.DV + v0 + v] = sS[d * 33 + v];
     }
 }
 
@@ -447,7 +450,8 @@ gdn_simt_out(GdnProblem p, const T* __restrict__ Q, const float* __restrict__ be
   for (int i = 0; i < 4; ++i)
     for (int j = 0; j < 4; ++j) {
       const int r = ty * 4 + i, v = v0 + tx * 4 + j;
-      if (r < n && v < p.DV) H[(at + r) * p.DV + v] = from_float<T>(p.scale * acc[i][j]);
+      if (r < n && v < p.DV && MLSTM_IN_BOUNDS(p, at + r < (long)p.BH * p.T))
+        H[(at + r) * p.DV + v] = from_float<T>(p.scale * acc[i][j]);
     }
 }
 
@@ -585,7 +589,7 @@ gdn_simt_grads(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
       for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 4; ++j) {
           const int r = ty * 4 + i, d = d0 + tn + j;
-          if (r >= n || d >= p.DK) continue;
+          if (r >= n || d >= p.DK || !MLSTM_IN_BOUNDS(p, t0 + r < p.T && bh < p.BH)) continue;
           const size_t at = ((size_t)(out32 ? (long)bh : kh) * p.T + t0 + r) * p.DK + d;
           if (out32)
             out32[at] = x[i][j];
@@ -651,7 +655,7 @@ gdn_simt_grads(GdnProblem p, const T* __restrict__ Q, const T* __restrict__ K,
     }
   }
   __syncthreads();
-  if (tid < n) {
+  if (tid < n && MLSTM_IN_BOUNDS(p, bh < p.BH && t0 + tid < p.T)) {
     dg[(long)bh * p.T + t0 + tid] = sent[tid];
     dbeta[(long)bh * p.T + t0 + tid] = sout[tid] + scol[tid] + sdiag[tid];
   }

@@ -133,7 +133,8 @@ gdn_step_kernel(GdnProblem p, const T* __restrict__ q, const T* __restrict__ k,
   auto put = [&](int r, float4 x) {
     float4 y = make_float4(a * x.x, a * x.y, a * x.z, a * x.w);
     fma4(y, sk[r], vn);
-    store4<kVec>(cp + (long)r * p.DV, left, y);
+    if (MLSTM_IN_BOUNDS(p, bh < p.BH && r < p.DK && (!kVec || left <= 0 || left >= 4)))
+      store4<kVec>(cp + (long)r * p.DV, left, y);
   };
 #pragma unroll
   for (int i = 0; i < kRows; ++i)

@@ -64,8 +64,8 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (wait) gdn_wait_stage();
     for (int v = 0; v < x.tiles; ++v)
       for (int t = 0; t < 2; ++t)
-        bulk_load(sa + (2 * t + v) * kBlk, w.S + ((x.cb * w.nvt + x.vt + v) * 2 + t) * kBlk,
-                  slabs * 8192, bar_in);
+        gdn_load(p, w, sa + (2 * t + v) * kBlk, w.S, 2 * w.nvt,
+                 (x.cb * w.nvt + x.vt + v) * 2 + t, slabs * 8192, bar_in);
   };
   auto load_v = [&](const GdnItem& x) {
     mbar_expect_tx(bar_v, x.tiles * kBlk);
@@ -210,8 +210,8 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     auto keep_y = [&] {
       for (int t = 0; t < x.tiles; ++t)
         for (int term = 0; term < 2; ++term)
-          bulk_store(w.y + ((x.cb * w.nvt + x.vt + t) * 2 + term) * kBlk,
-                     za + (2 * term + t) * kBlk, kBlk);
+          gdn_store(p, w, w.y, 2 * w.nvt, (x.cb * w.nvt + x.vt + t) * 2 + term,
+                    za + (2 * term + t) * kBlk, kBlk);
       tma_store_commit();
     };
     if (kH) {
@@ -255,7 +255,8 @@ gdn_tc_out_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (lead && rd.ok) {
       if (kH) {  // rows past T and columns past d_v are clipped
         for (int t = 0; t < x.tiles; ++t)
-          tma_store_3d(&tm_h, za + t * kBlk, (x.vt + t) * 64, x.t0, x.bh);
+          if (MLSTM_IN_BOUNDS(p, gdn_box_inside(p, (x.vt + t) * 64, p.DV, x.t0, x.bh, p.BH)))
+            tma_store_3d(&tm_h, za + t * kBlk, (x.vt + t) * 64, x.t0, x.bh);
         tma_store_commit();
       } else {
         keep_y();

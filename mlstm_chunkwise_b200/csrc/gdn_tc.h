@@ -168,6 +168,40 @@ __device__ __forceinline__ uint64_t mnmaj(uint32_t img, int kk) {
   return sdesc_sw128(img + kk * 2048, kBlk, 1024);
 }
 
+// Bulk copies of blocks of a workspace array with `per` blocks a chunk; debug builds
+// check them against its extent.
+__device__ __forceinline__ bool gdn_blocks_inside(const GdnProblem& p, const GdnTcWs& w, int per,
+                                                  size_t block, uint32_t bytes) {
+  return block * kBlk + bytes <= (size_t)p.BH * w.NC * per * kBlk;
+}
+__device__ __forceinline__ void gdn_load(const GdnProblem& p, const GdnTcWs& w, uint32_t dst,
+                                         const uint8_t* array, int per, size_t block,
+                                         uint32_t bytes, uint32_t bar) {
+  const bool in = MLSTM_IN_BOUNDS(p, gdn_blocks_inside(p, w, per, block, bytes));
+  bulk_load(dst, array + (in ? block * kBlk : 0), bytes, bar);
+}
+__device__ __forceinline__ void gdn_store(const GdnProblem& p, const GdnTcWs& w, uint8_t* array,
+                                          int per, size_t block, uint32_t src, uint32_t bytes) {
+  if (MLSTM_IN_BOUNDS(p, gdn_blocks_inside(p, w, per, block, bytes)))
+    bulk_store(array + block * kBlk, src, bytes);
+}
+// 32 columns of a row into an array of N's form.
+__device__ __forceinline__ void gdn_put_n(const GdnProblem& p, const GdnTcWs& w, float4* array,
+                                          size_t at, const uint32_t (&v)[32]) {
+  if (!MLSTM_IN_BOUNDS(p, at + 7 * 128 < (size_t)p.BH * w.NC * w.nvt * 16 * 128)) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    array[at + e * 128] =
+        make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                    __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+}
+// Debug builds: token t0, column c of head bh (of `heads`) is where a tensor store of an
+// array of `cols` columns may start.
+__device__ __forceinline__ bool gdn_box_inside(const GdnProblem& p, int c, int cols, int t0, int bh,
+                                               int heads) {
+  return c >= 0 && c < cols && t0 >= 0 && t0 < p.T && bh >= 0 && bh < heads;
+}
+
 // Two values to a bf16 pair, and what the rounding left of them.  (Conversions
 // of pairs: of single values they run at a quarter of the rate, which made a pass
 // that forms three terms of 128 x 128 values take 2700 cycles in place of 1400.)

@@ -34,13 +34,6 @@ constexpr uint32_t kZBar = kZCol + 1024;
 constexpr uint32_t kZSmem = kZBar + 64;
 static_assert(kZSmem <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ void put_n(float4* dst, const uint32_t (&v)[32]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    dst[e * 128] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                               __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-}
-
 __global__ void __launch_bounds__(kGdnThreads, 1)
 gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_dh, GdnProblem p,
@@ -224,7 +217,7 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (cols) {
       tmem_ld32(trow + 256, v);
       tmem_wait_ld();
-      put_n(w.dz0 + nb, v);
+      gdn_put_n(p, w, w.dz0, nb, v);
       put(-lam);
     }
     gdn_round(
@@ -244,7 +237,7 @@ gdn_tc_dz0_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (cols) {
       tmem_ld32(trow + 384, v);
       tmem_wait_ld();
-      put_n(w.N + nb, v);
+      gdn_put_n(p, w, w.N, nb, v);
     }
     x = nx;
   }
@@ -284,15 +277,15 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (wait) gdn_wait_stage();
     for (int v = 0; v < x.tiles; ++v)
       for (int t = 0; t < 3; ++t)
-        bulk_load(da + (2 * t + v) * kBlk, w.dS + ((x.cb * w.nvt + x.vt + v) * 3 + t) * kBlk,
-                  slabs * 8192, bar_in);
+        gdn_load(p, w, da + (2 * t + v) * kBlk, w.dS, 3 * w.nvt,
+                 (x.cb * w.nvt + x.vt + v) * 3 + t, slabs * 8192, bar_in);
   };
   auto load_y = [&](const GdnItem& x) {
     mbar_expect_tx(bar_y, x.tiles * 2 * kBlk);
     for (int v = 0; v < x.tiles; ++v)
       for (int t = 0; t < 2; ++t)
-        bulk_load(wa + (2 * t + v) * kBlk, w.y + ((x.cb * w.nvt + x.vt + v) * 2 + t) * kBlk, kBlk,
-                  bar_y);
+        gdn_load(p, w, wa + (2 * t + v) * kBlk, w.y, 2 * w.nvt,
+                 (x.cb * w.nvt + x.vt + v) * 2 + t, kBlk, bar_y);
   };
   uint4 ti[8];
   float2 ngc, ngl;
@@ -380,7 +373,8 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         put8(img, 2 * kBlk, r, (h & 1) * 4 + cc, a);
       }
-      w.out[ct * 256 + (h & 1) * 128 + r] = dec * o;
+      if (MLSTM_IN_BOUNDS(p, ct < (size_t)p.BH * w.NC * w.nvt))
+        w.out[ct * 256 + (h & 1) * 128 + r] = dec * o;
       const float4* zp = w.dz0 + (ct * 16 + (h & 1) * 8) * 128 + r;
 #pragma unroll
       for (int e = 0; e < 8; ++e) z0[e] = zp[e * 128];
@@ -408,11 +402,12 @@ gdn_tc_dz_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (lead) {  // every thread has read its part of dz0, which dz replaces
       for (int t = 0; t < x.tiles; ++t)
         for (int term = 0; term < 2; ++term)
-          bulk_store(w.dz + ((x.cb * w.nvt + x.vt + t) * 2 + term) * kBlk,
-                     wa + (2 * term + t) * kBlk, kBlk);
+          gdn_store(p, w, w.dz, 2 * w.nvt, (x.cb * w.nvt + x.vt + t) * 2 + term,
+                    wa + (2 * term + t) * kBlk, kBlk);
       if (rd.ok)  // rows past T and columns past d_v are clipped
         for (int t = 0; t < x.tiles; ++t)
-          tma_store_3d(&tm_dv, sbase + kYDv + t * kBlk, (x.vt + t) * 64, x.t0, x.bh);
+          if (MLSTM_IN_BOUNDS(p, gdn_box_inside(p, (x.vt + t) * 64, p.DV, x.t0, x.bh, p.BH)))
+            tma_store_3d(&tm_dv, sbase + kYDv + t * kBlk, (x.vt + t) * 64, x.t0, x.bh);
       tma_store_commit();
     }
     x = nx;
@@ -485,8 +480,8 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
   auto load_y = [&](size_t cb, int pr, uint32_t bar) {
     for (int v = 0; v < tiles_of(pr); ++v)
       for (int t = 0; t < 2; ++t)
-        bulk_load(ya + (2 * t + v) * kBlk, w.y + ((cb * w.nvt + 2 * pr + v) * 2 + t) * kBlk, kBlk,
-                  bar);
+        gdn_load(p, w, ya + (2 * t + v) * kBlk, w.y, 2 * w.nvt,
+                 (cb * w.nvt + 2 * pr + v) * 2 + t, kBlk, bar);
   };
   // dH, S and dz of a pair; y apart (its place may still hold results)
   auto load_a = [&](int it, int pr) {
@@ -497,8 +492,8 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
       const size_t ct = cb * w.nvt + 2 * pr + v;
       tma_load_3d(ha + v * kBlk, &tm_dh, (2 * pr + v) * 64, t0, bh, bar_a);
       for (int t = 0; t < 2; ++t) {
-        bulk_load(sa + (2 * t + v) * kBlk, w.S + (ct * 2 + t) * kBlk, sbytes, bar_a);
-        bulk_load(za + (2 * t + v) * kBlk, w.dz + (ct * 2 + t) * kBlk, kBlk, bar_a);
+        gdn_load(p, w, sa + (2 * t + v) * kBlk, w.S, 2 * w.nvt, ct * 2 + t, sbytes, bar_a);
+        gdn_load(p, w, za + (2 * t + v) * kBlk, w.dz, 2 * w.nvt, ct * 2 + t, kBlk, bar_a);
       }
     }
   };
@@ -507,8 +502,8 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
     mbar_expect_tx(bar_d, n * (2 * sbytes + (pairs > 1 ? 2 * kBlk : 0u)));
     for (int v = 0; v < n; ++v)
       for (int t = 0; t < 2; ++t)
-        bulk_load(za + (2 * t + v) * kBlk,
-                  w.dS + (((size_t)it * w.nvt + 2 * pr + v) * 3 + t) * kBlk, sbytes, bar_d);
+        gdn_load(p, w, za + (2 * t + v) * kBlk, w.dS, 3 * w.nvt,
+                 ((size_t)it * w.nvt + 2 * pr + v) * 3 + t, sbytes, bar_d);
     if (pairs > 1) load_y(it, pr, bar_d);
   };
   auto load_qk = [&](int it) {
@@ -853,7 +848,7 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int t = 4 * lane + e;
-            if (t < n) {
+            if (t < n && MLSTM_IN_BOUNDS(p, bh < p.BH && t0 + t < p.T)) {
               dg[(long)bh * p.T + t0 + t] = y[e] + before;
               dbeta[(long)bh * p.T + t0 + t] = o[e] + cs[e] + sdiag[t];
             }
@@ -896,7 +891,9 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
         constexpr int kW = kShared ? 32 : 64, kN = kShared ? 4 : 2;
         for (int m = 0; m < 2; ++m)
           for (int b = 0; b * kW < p.DK; ++b)
-            tma_store_3d(m ? &tm_dk : &tm_dq, ya + (kN * m + b) * kBlk, b * kW, t0, hd);
+            if (MLSTM_IN_BOUNDS(p, gdn_box_inside(p, b * kW, p.DK, t0, hd,
+                                                  kShared ? p.BH : p.B * p.NHK)))
+              tma_store_3d(m ? &tm_dk : &tm_dq, ya + (kN * m + b) * kBlk, b * kW, t0, hd);
         tma_store_commit();
         if (more && !kShared) load_a(next, 0);
         tma_store_wait_read_all();

@@ -74,10 +74,9 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
         if (i >= 2) ok = mbar_wait(bar(kMFree0 + b), ((i >> 1) - 1) & 1, wt, 0x51);
         if (!ok) break;
         mbar_expect_tx(bar(kMFull0 + b), 2 * slabs * kBlk);
-        const uint8_t* src = w.M + chunk(i) * 4 * kBlk;
         for (int t = 0; t < 2; ++t)
-          bulk_load(sbase + kOffM + (4 * b + 2 * t) * kBlk, src + t * 2 * kBlk, slabs * kBlk,
-                    bar(kMFull0 + b));
+          gdn_load(p, w, sbase + kOffM + (4 * b + 2 * t) * kBlk, w.M, 4, chunk(i) * 4 + 2 * t,
+                   slabs * kBlk, bar(kMFull0 + b));
       }
       // every load has landed before the CTA exits
       for (int i = steps > 2 ? steps - 2 : 0; ok && i < steps; ++i)
@@ -106,9 +105,9 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
           mma_commit(bar(kX));
           mma_commit(bar(kMFree0 + b));
         }
-        uint8_t* dst = (kRev ? w.dS : w.S) + (chunk(i) * w.nvt + vt) * kTerms * kBlk;
         for (int t = 0; t < kTerms; ++t)
-          bulk_store(dst + t * kBlk, sa + t * kBlk, slabs * 8192);
+          gdn_store(p, w, kRev ? w.dS : w.S, kTerms * w.nvt, (chunk(i) * w.nvt + vt) * kTerms + t,
+                    sa + t * kBlk, slabs * 8192);
         tma_store_commit();
       }
       tma_store_wait_all();
@@ -165,7 +164,7 @@ gdn_tc_chain_kernel(GdnProblem p, const float* __restrict__ init, float* __restr
     if (fin && ok && r < p.DK)
 #pragma unroll
       for (int e = 0; e < 16; e += 4)  // DV is a multiple of 8
-        if (v0 + e < p.DV)
+        if (v0 + e < p.DV && MLSTM_IN_BOUNDS(p, bh < p.BH && v0 + e + 4 <= p.DV))
           *reinterpret_cast<float4*>(fin + ((long)bh * p.DK + r) * p.DV + v0 + e) =
               make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
   }

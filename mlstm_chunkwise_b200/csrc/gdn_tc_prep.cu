@@ -287,7 +287,8 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
       for (int k = 0; k < 4; ++k) {
         const uint4 uh = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
         const uint4 ul = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
-        if (b <= q) {
+        if (b <= q && MLSTM_IN_BOUNDS(p, (size_t)i * 32 * 128 + r + (16 + b * 4 + k) * 128 <
+                                             (size_t)p.BH * w.NC * 32 * 128)) {
           dst[(b * 4 + k) * 128] = uh;
           dst[(16 + b * 4 + k) * 128] = ul;
         }
@@ -309,7 +310,8 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
             ia + (term * 2 + (sb >> 3)) * kBlk + sw128_offset(rg * 32 + lane, sb & 7), v);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          out[((term * 16 + rg * 4 + m) * 128 + sb * 8 + (lane >> 2)) * 4 + (lane & 3)] = v[m];
+          if (MLSTM_IN_BOUNDS(p, term * 16 + rg * 4 + m < 32 && sb * 8 + (lane >> 2) < 128))
+            out[((term * 16 + rg * 4 + m) * 128 + sb * 8 + (lane >> 2)) * 4 + (lane & 3)] = v[m];
       }
       __syncthreads();  // the diagonal blocks' place is read
     }
@@ -507,11 +509,7 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       if (h < 2 * x.tiles) {
         tmem_ld32(trow + 256, v);
         tmem_wait_ld();
-        float4* dst = w.N + ((x.cb * w.nvt + x.vt + (h >> 1)) * 16 + (h & 1) * 8) * 128 + r;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dst[e * 128] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                     __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+        gdn_put_n(p, w, w.N, ((x.cb * w.nvt + x.vt + (h >> 1)) * 16 + (h & 1) * 8) * 128 + r, v);
       }
     }
     fence_proxy_async_smem();
@@ -519,7 +517,7 @@ gdn_tc_mn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __syncthreads();
     if (lead && first) {
       for (int t = 0; t < 2; ++t)
-        bulk_store(w.M + (x.cb * 4 + 2 * t) * kBlk, wa + 2 * t * kBlk, slabs * kBlk);
+        gdn_store(p, w, w.M, 4, x.cb * 4 + 2 * t, wa + 2 * t * kBlk, slabs * kBlk);
       tma_store_commit();
     }
     x = nx;

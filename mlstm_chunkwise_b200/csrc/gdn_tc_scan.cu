@@ -216,7 +216,8 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
       sync();  // H
       if (lead && ok) {  // rows past T and columns past d_v are clipped
         for (int t = 0; t < tiles; ++t)
-          tma_store_3d(&tm_h, za + t * kBlk, (vt + t) * 64, c * kGdnL, bh);
+          if (MLSTM_IN_BOUNDS(p, gdn_box_inside(p, (vt + t) * 64, p.DV, c * kGdnL, bh, p.BH)))
+            tma_store_3d(&tm_h, za + t * kBlk, (vt + t) * 64, c * kGdnL, bh);
         tma_store_commit();
       }
       __syncwarp();
@@ -333,7 +334,7 @@ gdn_tc_scan_kernel(const __grid_constant__ CUtensorMap tm_q,
           float* dst = C_T + ((long)bh * p.DK + r) * p.DV + v0;
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            if (v0 + e < p.DV)
+            if (v0 + e < p.DV && MLSTM_IN_BOUNDS(p, bh < p.BH && v0 + e + 4 <= p.DV))
               *reinterpret_cast<float4*>(dst + e) =
                   make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
                               __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));

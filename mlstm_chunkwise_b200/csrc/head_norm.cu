@@ -205,10 +205,11 @@ head_norm_fw_kernel(HeadNormProblem p, const T* __restrict__ X,
       if (c < p.D) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) v[i][e] = fmaf(v[i][e] * r, w[i][e], b[i][e]);
-        Vec<T, kVec>::store(y + c, v[i]);
+        if (MLSTM_IN_BOUNDS(p, at.b < p.B && at.t < p.T && c + kVec <= p.D))
+          Vec<T, kVec>::store(y + c, v[i]);
       }
     }
-    if (lane == 0) {
+    if (lane == 0 && MLSTM_IN_BOUNDS(p, xr < (long)p.B * p.NH * p.T)) {
       if (mean) mean[xr] = mu;
       if (rstd) rstd[xr] = r;
     }
@@ -320,7 +321,8 @@ head_norm_bw_kernel(HeadNormProblem p, const T* __restrict__ X,
       if (c < p.D) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) av[i][e] = r * (av[i][e] - s0 - xv[i][e] * s1);
-        Vec<T, kVec>::store(dx + c, av[i]);
+        if (MLSTM_IN_BOUNDS(p, xr < (long)p.B * p.NH * p.T && c + kVec <= p.D))
+          Vec<T, kVec>::store(dx + c, av[i]);
       }
     }
   }

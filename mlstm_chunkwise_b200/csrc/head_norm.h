@@ -8,6 +8,7 @@ namespace mlstm {
 struct HeadNormProblem {
   int B, NH, T, D;
   float eps;
+  uint32_t* err;  // of the bounds-checked build (else nullptr)
 };
 
 constexpr int kHeadNormMaxD = 8192;

@@ -211,3 +211,39 @@ def test_norm_behind_the_mlstm():
     H2, _ = api.mlstm_chunkwise(*leaves)
     want = (*torch.autograd.grad(H2, leaves, d["dX"]), d["dweight"], d["dbias"])
     assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+@pytest.fixture(scope="module")
+def dbg():
+    from mlstm_chunkwise_b200 import build
+    return _lib.open_library(build.build(debug_bounds=True))
+
+
+@pytest.mark.parametrize("algo,dtype,size", CASES, ids=str)
+def test_bounds_checked_build(dbg, monkeypatch, algo, dtype, size):
+    """Its checks of workspace copies and stores find nothing and change no bit."""
+    B, NHK, NH, T, DK, DV = size
+    x, a, dH, dC = inputs(dtype, size, True)
+    w = torch.ones(NH, DV, device="cuda")
+    pair = algo == "tc" and B * NH * T >= 64
+
+    def work():
+        H, C = api.gated_delta_fw(*a, algo=algo)
+        out = [H, C, *api.gated_delta_bw(*a[:5], dH, x["C0"], dC, algo=algo).values()]
+        if pair:
+            H, C, saved = api.gated_delta_fw_train(*a)
+            out += [H, C, *api.gated_delta_bw_saved(*a[:5], saved, dH, x["C0"], dC).values()]
+        C = C.clone()
+        out += [api.gated_delta_step(*(t[:, :, -1].contiguous() for t in a[:5]), C), C]
+        Y, mean, rstd = api.head_norm_fw(H, w, w)
+        return out + [Y, mean, rstd, *api.head_norm_bw(H, Y, w, mean, rstd).values()]
+
+    want = work()
+    torch.cuda.synchronize()
+    dbg.mlstm_set_watchdog(1 << 22)
+    monkeypatch.setattr(_lib, "_lib", dbg)
+    got = work()
+    torch.cuda.synchronize()
+    assert dbg.mlstm_last_device_error(None) == _lib.OK
+    assert dbg.mlstm_last_device_error_word() == 0
+    assert all(torch.equal(u, v) for u, v in zip(got, want))
