@@ -290,7 +290,8 @@ mlstm_status mlstm_step(const void* q, const void* k, const void* v, const float
  * Contiguous; 16-byte aligned but for g, beta and their gradients (4 bytes).
  * Sizes: B, NHK, NH >= 1, T >= 0 (up to 2^22), DK, DV in [1, 1024], B * NH up
  * to 65535.  T = 0 copies C0 (or zero) to C_T.
- * Algorithms: SIMT (any size and type, fp32 throughout) and TC (bf16, DK up to
+ * Algorithms: SIMT (any size and type, fp32 on the CUDA cores: 3 to 7 times the
+ * time) and TC (bf16, DK up to
  * 128, DK and DV multiples of 8; tensor cores, every fp32 operand split into
  * two or three bf16 terms so that fp32 outputs keep about 17 bits); AUTO takes
  * TC where it applies, but SIMT for the gradients of fewer than 64 tokens over
@@ -321,9 +322,10 @@ mlstm_status mlstm_gated_delta_bw(const void* Q, const void* K, const void* V, c
                                   int DV, float scale, mlstm_dtype dtype, mlstm_algo algo,
                                   void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
 
-/* Training pair: mlstm_gated_delta_fw_train is the forward that also keeps, in a caller buffer `saved`, what it formed per 128
- * tokens (sums of g, inverses, transition matrices, states and y, about 2.1 KB
- * per token and head at DK = DV = 128); mlstm_gated_delta_bw_saved is
+/* Training pair: mlstm_gated_delta_fw_train is the forward that also keeps, in a
+ * caller buffer `saved`, what it formed per 128 tokens (sums of g, inverses,
+ * transition matrices, states and y, about 2.1 KB per token and head at
+ * DK = DV = 128); mlstm_gated_delta_bw_saved is
  * mlstm_gated_delta_bw from it, without recomputing the forward.  `saved` must
  * not change between the two calls.  Only where AUTO takes the tensor cores for
  * the gradients (else MLSTM_ERR_UNSUPPORTED, from

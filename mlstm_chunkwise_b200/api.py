@@ -465,10 +465,12 @@ def gated_delta_fw(Q, K, V, g, beta, C0=None, *, scale: float | None = None, alg
     Padded tokens with g = beta = 0 (and finite q, k, v) leave the state as it
     was.  A reset at the first token forgets C0 whatever it holds; elsewhere an
     infinity or a NaN reaches all of its head from its chunk on (64 or 128 tokens),
-    behind resets and padding too.  Returns ``(H, C_T)``, or ``H`` without ``return_last_state``.  ``out``
-    may hold preallocated ``H`` / ``C_T`` (C_T may be C0 itself); ``workspace`` a
-    uint8 CUDA tensor of at least ``gated_delta_workspace_size(...)`` bytes.
-    ``algo``: "auto", "simt" or "tc".
+    behind resets and padding too.  Returns ``(H, C_T)``, or ``H`` without
+    ``return_last_state``.  ``out`` may hold preallocated ``H`` / ``C_T`` (C_T may
+    be C0 itself); ``workspace`` a uint8 CUDA tensor of at least
+    ``gated_delta_workspace_size(...)`` bytes.  ``algo``: "auto", "simt" (fp32 on
+    the CUDA cores: what "auto" takes for float32, DK above 128, or DK or DV that
+    are no multiples of 8; 3 to 7 times the time) or "tc".
     """
     if Q.dim() != 4:
         raise ValueError("Q must be [B, NHK, T, DK] and V [B, NH, T, DV]")
@@ -609,8 +611,8 @@ def gated_delta_bw_saved(Q, K, V, g, beta, saved, dH, C0=None, dC_T=None, *,
 def gated_delta_step(q, k, v, g, beta, C, *, scale: float | None = None, h=None):
     """One token of ``gated_delta_fw`` for every (b, head), in place on the
     state: q, k [B,NHK,DK], v [B,NH,DV], g, beta [B,NH] float32, C [B,NH,DK,DV]
-    float32 (overwritten).  Returns h [B,NH,DV] in the input dtype (``h`` may be
-    given)."""
+    float32 (overwritten; a g of -inf forgets it whatever it holds).  Returns h
+    [B,NH,DV] in the input dtype (``h`` may be given)."""
     B, NHK, NH, DK, DV, dev, dt = _check_gated_delta(q, k, v, g, beta, C, ())
     given = h
     if h is None:

@@ -20,9 +20,13 @@
 // bf16 rounding of the state or of the inverse would put 2e-3 of noise on
 // every output, and dg, a difference of large sums, off by percents.  Where one
 // rounding alone would set the error of an fp32 output, the operand has a third
-// term (24 bits) or the sum is taken in fp32: the last operands of N and N'
-// (final state, dC0), the gradient of the state in K dS', and y against it
-// (dbeta, dg).
+// term (24 bits) or the sum is taken in fp32: the last operands of N and N' and what
+// the fused forward writes to the state (final state, dC0), the gradient of the state
+// in K dS', and y against it (dbeta, dg).  In y dS'^T (a term of the bf16 dK) and in
+// <S, dS'> (beside S, which has two) the gradient of the state enters with its first
+// two terms.  Exponentials are ex2.approx (2^-22 of the value) with the exponent's
+// rounding carried along, quotients of them __fdividef (2^-22): a quarter of 2^-20 at
+// most, an order below two terms.
 #pragma once
 
 #include "device_address.h"
@@ -359,7 +363,9 @@ struct GdnItem {
   size_t cb;
   int bh, t0, n, vt, tiles;
   __device__ GdnItem(long i, const GdnProblem& p, const GdnTcWs& w) {
-    const int pairs = (w.nvt + 1) / 2;  // each item has 160 KB of workspace or more: an int holds them
+    // an int holds the items: up to 65535 heads and 2^15 chunks do in any case, and
+    // with pairs of value tiles each item has 136 KB of workspace or more
+    const int pairs = (w.nvt + 1) / 2;
     const int k = (int)i, c = k / pairs;
     cb = (size_t)c;
     vt = (k - c * pairs) * 2;

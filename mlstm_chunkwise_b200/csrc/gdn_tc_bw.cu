@@ -497,7 +497,8 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
     }
   };
-  auto load_d = [&](int it, int pr) {  // dS' (and y again, where there are several pairs)
+  // the first two terms of dS' (and y again, where there are several pairs)
+  auto load_d = [&](int it, int pr) {
     const int n = tiles_of(pr);
     mbar_expect_tx(bar_d, n * (2 * sbytes + (pairs > 1 ? 2 * kBlk : 0u)));
     for (int v = 0; v < n; ++v)
@@ -591,7 +592,7 @@ gdn_tc_grads_kernel(const __grid_constant__ CUtensorMap tm_q,
             }
           },
           [&] {
-            // both states' images, in whatever order: 16-byte pieces of both terms
+            // both states' images, in whatever order: 16-byte pieces of two terms
             for (int v = 0; v < nt; ++v) {
               const size_t ct = (size_t)it * w.nvt + 2 * pr + v;
               const uint4* s0 = reinterpret_cast<const uint4*>(w.S + ct * 2 * kBlk);

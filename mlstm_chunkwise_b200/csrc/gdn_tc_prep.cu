@@ -51,7 +51,7 @@ gdn_tc_inverse_kernel(const __grid_constant__ CUtensorMap tm_k, GdnProblem p,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, h = warp >> 2, r = q * 32 + lane;
   const int slabs = (p.DK + 63) / 64;
-  const int items = p.BH * w.NC;  // each has 160 KB of workspace or more: an int holds them
+  const int items = p.BH * w.NC;  // up to 65535 x 2^15: an int holds them and a grid more
   const Problem wt{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.f, 0, p.err, p.max_polls};
   // item i: chunk i % NC of head i / NC, so rows i * 128 of the workspace's arrays
   auto load_k = [&](int i) {
@@ -537,10 +537,10 @@ cudaError_t launch_gdn_tc_inverse(const GdnProblem& p, const GdnInputs& x, const
   const long items = (long)p.BH * w.NC;
   const dim3 grid((unsigned)(items < 2 * kGdnSms ? items : 2 * kGdnSms));
   if (w.tinvt)
-    return gdn_launch(&gdn_tc_inverse_kernel<true>, grid, kInvThreads, inv_smem(true), false, st, m.k, p,
-                      x.g, x.beta, w);
-  return gdn_launch(&gdn_tc_inverse_kernel<false>, grid, kInvThreads, inv_smem(false), false, st, m.k, p,
-                    x.g, x.beta, w);
+    return gdn_launch(&gdn_tc_inverse_kernel<true>, grid, kInvThreads, inv_smem(true), false, st,
+                      m.k, p, x.g, x.beta, w);
+  return gdn_launch(&gdn_tc_inverse_kernel<false>, grid, kInvThreads, inv_smem(false), false, st,
+                    m.k, p, x.g, x.beta, w);
 }
 
 cudaError_t launch_gdn_tc_mn(const GdnProblem& p, const GdnInputs& x, const GdnMaps& m,
