@@ -58,6 +58,13 @@ def _written(*tensors):
 _written_one = torch.autograd.graph.increment_version  # half a microsecond less
 
 
+def _upstream(grad):
+    """An upstream gradient as the kernels take it: autograd may hand on a view with
+    strides, or a slice that starts off a 16-byte boundary."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 def workspace_size(B, NH, T, DK, DV, chunk_size, dtype=torch.bfloat16, algo="auto") -> int:
     n = ctypes.c_size_t(0)
     _lib.check(_lib.lib().mlstm_fw_workspace_size(B, NH, T, DK, DV, chunk_size, _DT[dtype],
@@ -377,11 +384,11 @@ class _MlstmChunkwise(torch.autograd.Function):
         chunk_size, gate_mode, kept = ctx.cfg
         if kept:
             Q, K, V, i_pre, f_pre, C0, n0, m0, H, saved = ctx.saved_tensors
-            g = mlstm_bw_saved(Q, K, V, i_pre, f_pre, H, saved, dH.contiguous(), C0, n0, m0,
+            g = mlstm_bw_saved(Q, K, V, i_pre, f_pre, H, saved, _upstream(dH), C0, n0, m0,
                                gate_mode=gate_mode)
         else:
             Q, K, V, i_pre, f_pre, C0, n0, m0 = ctx.saved_tensors
-            g = mlstm_bw(Q, K, V, i_pre, f_pre, dH.contiguous(), C0, n0, m0,
+            g = mlstm_bw(Q, K, V, i_pre, f_pre, _upstream(dH), C0, n0, m0,
                          chunk_size=chunk_size, gate_mode=gate_mode)
         return (g["dQ"], g["dK"], g["dV"], g["di_pre"], g["df_pre"], g.get("dC0"), g.get("dn0"),
                 g.get("dm0"), None, None, None, None)
@@ -653,8 +660,8 @@ class _GatedDelta(torch.autograd.Function):
             return (None,) * 9
         Q, K, V, g, beta, C0, saved = ctx.saved_tensors
         scale, algo = ctx.cfg
-        dH = torch.zeros_like(V) if dH is None else dH.contiguous()
-        dC_T = None if dC_T is None else dC_T.contiguous()
+        dH = torch.zeros_like(V) if dH is None else _upstream(dH)
+        dC_T = None if dC_T is None else _upstream(dC_T)
         if saved is not None:
             d = gated_delta_bw_saved(Q, K, V, g, beta, saved, dH, C0, dC_T, scale=scale)
         else:
@@ -761,10 +768,11 @@ class _HeadNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         X, weight, mean, rstd = ctx.saved_tensors
-        d = head_norm_bw(X, dY.contiguous(), weight, mean, rstd, bias=ctx.has_bias)
+        d = head_norm_bw(X, _upstream(dY), weight, mean, rstd, bias=ctx.has_bias)
         return d["dX"], d["dweight"], d.get("dbias"), None
 
 
 def head_norm(X, weight, bias=None, *, eps: float = 1e-5):
-    """``head_norm_fw`` that autograd can differentiate; returns Y."""
+    """``head_norm_fw`` that autograd can differentiate; returns Y.  (Capture of a
+    backward pass: as ``gated_delta_chunkwise``.)"""
     return _HeadNorm.apply(X, weight, bias, eps)
