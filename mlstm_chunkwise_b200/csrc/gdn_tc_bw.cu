@@ -8,7 +8,7 @@
 // one chunk's operands with six 128 x 128 accumulators in turn in all of the
 // tensor memory: 184 products of 128 x 128 x 16 for 128 value columns.
 //
-// 1024 chunks of 128 x 128: dz0 89 us (88 products, four rounds: bound by the
+// 1024 chunks of 128 x 128: dz0 94 us (88 products, four rounds: bound by the
 // rounds' latency), dz 81 us (390 KB an item, HBM at 4.5 TB/s), grads 199 us (28 us
 // an item: about 9 wait for the item's 224 KB of tiles, which fill the shared
 // memory that a prefetch would need, and 7 are products).  Loading the 128 KB for

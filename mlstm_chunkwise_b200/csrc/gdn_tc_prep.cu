@@ -19,7 +19,7 @@ using namespace tc;
 // terms (A21 and T22 in tensor memory, T11 and A21 T11 as images).  Half a dozen
 // dependent passes of little work each, bound by their latency: two blocks share
 // an SM, and the next item's K, its K K^T and its sums are prepared meanwhile
-// (8192 chunks 208 us, 512 chunks 21; a block per item 262 and 22).  What costs
+// (8192 chunks 208 to 220 us, 512 chunks 21; a block per item 262 and 22).  What costs
 // beyond that is instruction fetch, so loops whose copies would differ in little
 // stay rolled, and anything in local memory, for which the shared memory leaves
 // little L1 (a row's diagonal bit cleared by index, not by mask: 293 us).
